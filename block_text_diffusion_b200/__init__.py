@@ -12,6 +12,9 @@ import ctypes
 import os
 
 from . import inputs  # noqa: F401  (seeded synthetic inputs)
+from . import serving
+from .serving import (HeadNorm, PagedBatch, PagedKV, Rope, paged_append, paged_attention,  # noqa: F401
+                      paged_attention_workspace, qk_norm_rope, rope_frequencies)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")
@@ -93,6 +96,7 @@ def lib():
             "dg_test_launch_shape": ([I32, I64, I32, I32, P], I32),
             "dg_touched_experts_sum": ([P, P, I32, P], I32),
             "dg_gemm_splitk_noalloc": ([P, P, P, I32, I32, I32, I32, P], I32),
+            **serving.signatures(),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)

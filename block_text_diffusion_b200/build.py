@@ -15,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = sorted(glob.glob(os.path.join(HERE, "csrc", "*"))) + sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
+UNITS = ("dg_engine.cu", "dg_noalloc.cu", "dg_serve.cu")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -37,7 +38,7 @@ def build(force: bool = False, verbose: bool = False, lib: str = LIB) -> str:
         return lib
     tmp = lib + ".tmp%d" % os.getpid()
     cmd = [nvcc(), "-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC", "-shared",
-           "-o", tmp, os.path.join(HERE, "csrc", "dg_engine.cu"), os.path.join(HERE, "csrc", "dg_noalloc.cu")]
+           "-o", tmp, "--threads", "0", *(os.path.join(HERE, "csrc", f) for f in UNITS)]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.check_call(cmd)

@@ -1,0 +1,58 @@
+// What the paged serving operators share: the ragged batch as kernels see it.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dg_device.cuh"
+
+// The caller's arrays are device memory the host never looks at, so every
+// value read from them is brought into range before it is used as an index
+// and reported through the status word when it was out of range.
+struct PagedBatch {
+  int n_seqs, n_tokens;
+  const int* cu_q;
+  const int* kv_lens;
+  const int* table;
+  long long table_stride;
+  int max_pages;
+  const int* prefix_pages;
+  int prefix_len;
+  int n_pages, page_shift;   // page size = 1 << page_shift
+  int* status;
+};
+
+struct PagedSeq {
+  int q0, nq;   // rows of the token buffers
+  int kv;       // own tokens in the cache, the new ones included
+};
+
+// status word values: dg_status codes of include/dg.h
+constexpr int kStatusTimeout = 4;   // DG_ERR_TIMEOUT
+constexpr int kStatusState = 5;     // DG_ERR_STATE
+
+#define DG_HD __host__ __device__ __forceinline__
+
+DG_HD int imin(int a, int b) { return a < b ? a : b; }
+DG_HD int imax(int a, int b) { return a > b ? a : b; }
+DG_HD long long lmin(long long a, long long b) { return a < b ? a : b; }
+DG_HD long long lmax(long long a, long long b) { return a > b ? a : b; }
+
+DG_HD void paged_error(const PagedBatch& b, int code) {
+#ifdef __CUDA_ARCH__
+  dev_error(b.status, code);
+#else
+  if (b.status && *b.status == 0) *b.status = code;
+#endif
+}
+
+DG_HD PagedSeq paged_seq(const PagedBatch& b, int i) {
+  const int a0 = b.cu_q[i], a1 = b.cu_q[i + 1], kv = b.kv_lens[i];
+  PagedSeq s;
+  s.q0 = imin(imax(a0, 0), b.n_tokens);
+  const int q1 = imin(imax(a1, s.q0), b.n_tokens);
+  s.nq = q1 - s.q0;
+  const long long room = (long long)b.max_pages << b.page_shift;
+  s.kv = (int)lmin(imax(kv, 0), room);
+  if (s.q0 != a0 || q1 != a1 || s.kv != kv) paged_error(b, kStatusState);
+  return s;
+}

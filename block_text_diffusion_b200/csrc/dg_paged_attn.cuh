@@ -1,0 +1,500 @@
+// Attention of ragged queries over a paged cache with a prefix the whole
+// batch shares:
+//
+//   out_r = sum_j softmax_j(scale q_r.k_j) v_j,   lse_r = ln sum_j exp(scale q_r.k_j)
+//
+// over the prefix's keys and the sequence's own.  Softmax over a union of key
+// sets splits exactly: with per-set lse_i and normalised out_i,
+// lse = ln sum_i exp(lse_i) and out = sum_i exp(lse_i - lse) out_i.  So the
+// prefix is one attention problem whose query rows are the whole batch's (its
+// keys are read once, and 64 single tokens fill a matrix tile together), every
+// sequence's own keys are another, and any tile may be cut along its keys.
+//
+// Work.  For one key head, the rows (token, query head of the group) of a
+// sequence are cut into tiles of kRows rows, and each tile has the key blocks
+// its rows can see.  All (part, sequence, key head, tile, key block) units lie
+// on one line; CTA c takes the c-th of equal intervals of it.  A CTA so gets
+// the end of one tile, whole tiles, and the start of another, whatever the
+// lengths are, and no length has to be known on the host.  A tile that lies in
+// one interval goes straight to the output; of a cut tile the CTA holding its
+// first block keeps its result by row, the others in a slot of their own, and
+// a second kernel joins them in order (the sums never depend on timing).
+#pragma once
+#include "dg_paged.cuh"
+
+struct PagedAttnArgs {
+  PagedBatch b;
+  const void* q;
+  void* out;
+  long long q_ts, q_hs, o_ts, o_hs;   // token and head strides, elements
+  int n_heads, n_kv_heads, G;         // G = n_heads / n_kv_heads
+  int causal;
+  float scale_log2;                   // scale * log2(e)
+  const void *k_pages, *v_pages;
+  float* lse;                         // natural, [n_tokens][n_heads], or null
+  // workspace (rows = n_tokens * n_heads; parts: 0 own keys, 1 the prefix)
+  int2* meta;                         // [parts][rows]: see PagedFrag::meta
+  float* part_lse;                    // [parts][rows] log2-sum-exp of a cut tile's first piece
+  float* slot_lse;                    // [grid][kRows]
+  float* part_o;                      // [parts][rows][hd] normalised
+  float* slot_o;                      // [grid][kRows][hd]
+};
+
+// One piece of work of a CTA: key blocks [kb0, kb1) of a tile.
+struct PagedFrag {
+  int nblk;        // key blocks; 0: no more work
+  int part;        // 0: own keys, 1: the prefix
+  int q0;          // first token of the sequence (part 1: of the batch)
+  int row0, rows;  // the tile's first row of the sequence (row = token * G + head in group), its rows
+  int kvh;         // key head
+  int kb0;
+  int limit;       // keys the tile's last row can see
+  int vis0;        // row r sees the keys below min(vis_max, vis0 + (row0 + r) / G)
+  int vis_max;
+  int pages;       // needed entries of the page list
+  int first;       // the piece starts its tile
+  int whole;       // the piece is the whole tile
+  int n_cont;      // later CTAs that hold pieces of this tile (valid where first)
+  const int* page_list;
+};
+
+template <int kRows, int kBlk>
+struct PagedWalk {
+  const PagedAttnArgs& a;
+  long long x, x1;          // interval left: [x, x1)
+  long long per;            // interval length
+  // current tile
+  int part, seq, kvh, tile;
+  long long tile_x0;        // where the current tile starts on the line
+  PagedSeq s;               // the sequence (part 1: the whole batch over the prefix)
+
+  DG_HD PagedWalk(const PagedAttnArgs& a_) : a(a_) {}
+
+  DG_HD int tiles_of(const PagedSeq& q) const { return (int)(((long long)q.nq * a.G + kRows - 1) / kRows); }
+  // keys visible to the last row of a tile of the current sequence
+  DG_HD int tile_limit(const PagedSeq& q, int part_, int tl) const {
+    if (part_ == 1 || !a.causal) return q.kv;
+    const long long last = lmin((long long)(tl + 1) * kRows, (long long)q.nq * a.G) - 1;
+    return imax(0, q.kv - q.nq + (int)(last / a.G) + 1);
+  }
+  // A tile whose rows see nothing keeps one (masked) block: it writes its zeros.
+  DG_HD int tile_blocks(const PagedSeq& q, int part_, int tl) const {
+    return imax(1, (int)(((long long)tile_limit(q, part_, tl) + kBlk - 1) / kBlk));
+  }
+  // key blocks of all tiles of one sequence for one key head
+  DG_HD long long seq_blocks(const PagedSeq& q, int part_) const {
+    const int n = tiles_of(q);
+    if (part_ == 1 || !a.causal) return (long long)n * tile_blocks(q, part_, 0);
+    long long sum = 0;
+    for (int i = 0; i < n; ++i) sum += tile_blocks(q, part_, i);
+    return sum;
+  }
+  DG_HD PagedSeq whole_batch() const {
+    const PagedBatch& b = a.b;
+    PagedSeq p;
+    const int lo = b.n_seqs > 0 ? b.cu_q[0] : 0, hi = b.n_seqs > 0 ? b.cu_q[b.n_seqs] : 0;
+    p.q0 = imin(imax(lo, 0), b.n_tokens);
+    p.nq = imin(imax(hi, p.q0), b.n_tokens) - p.q0;
+    p.kv = b.prefix_len;
+    return p;
+  }
+  DG_HD long long prefix_blocks() const {
+    return a.b.prefix_len > 0 ? seq_blocks(whole_batch(), 1) * a.n_kv_heads : 0;
+  }
+  // Interval `cta` of `grid` equal ones of a line of `total` blocks; false if it is empty.
+  DG_HD bool take_interval(long long total, int cta, int grid) {
+    per = lmax(1, (total + grid - 1) / grid);
+    x = lmin(total, cta * per);
+    x1 = lmin(total, x + per);
+    return x < x1;
+  }
+  DG_HD void enter_prefix() {
+    part = 1;
+    seq = -1;
+    s = whole_batch();
+    const long long each = seq_blocks(s, 1), nb = tile_blocks(s, 1, 0);
+    kvh = (int)(x / each);
+    tile = (int)(x % each / nb);
+    tile_x0 = kvh * each + tile * nb;
+  }
+  // x lies in sequence i, which starts at x0 on the line
+  DG_HD void enter_sequence(int i, long long x0) {
+    part = 0;
+    seq = i;
+    s = paged_seq(a.b, i);
+    const long long each = lmax(1, seq_blocks(s, 0));
+    kvh = (int)lmin(a.n_kv_heads - 1, (x - x0) / each);
+    tile = 0;
+    tile_x0 = x0 + kvh * each;
+    const int n = tiles_of(s);
+    for (int nb; tile + 1 < n && x >= tile_x0 + (nb = tile_blocks(s, 0, tile)); ++tile) tile_x0 += nb;
+  }
+
+  // Finds the CTA's interval and where it starts; called by all kThreads
+  // threads of the CTA, which share `tmp` and `found`.  Every thread adds up a
+  // run of sequences and the runs are scanned, so the lengths are read once
+  // per CTA.  False (for every thread): there is nothing to do.
+  template <int kThreads>
+  __device__ bool begin(long long (&tmp)[kThreads / 32 + 1], int& found) {
+    const PagedBatch& b = a.b;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int run = (b.n_seqs + kThreads - 1) / kThreads;
+    const int i0 = min(b.n_seqs, (int)threadIdx.x * run), i1 = min(b.n_seqs, i0 + run);
+    long long sum = 0;
+    for (int i = i0; i < i1; ++i) sum += seq_blocks(paged_seq(b, i), 0);
+    sum *= a.n_kv_heads;
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) tmp[warp] = incl;
+    if (threadIdx.x == 0) found = -1;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) before += tmp[i];
+      total += tmp[i];
+    }
+    incl += before;
+    const long long pre = prefix_blocks();
+    if (!take_interval(total + pre, blockIdx.x, gridDim.x)) return false;
+    if (x < pre) {
+      enter_prefix();
+      return true;
+    }
+    // the thread whose run holds x names the sequence and where it starts
+    const long long y = x - pre;
+    if (y >= incl - sum && y < incl) {
+      long long at = incl - sum;
+      for (int i = i0; i < i1; ++i) {
+        const long long n = seq_blocks(paged_seq(b, i), 0) * a.n_kv_heads;
+        if (y < at + n) {
+          found = i;
+          tmp[kThreads / 32] = pre + at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    if (found < 0) return false;   // (lengths that change while the kernel runs)
+    enter_sequence(found, tmp[kThreads / 32]);
+    return true;
+  }
+
+  // The same on the host, for a batch in host memory.
+  bool begin_host(int cta, int grid) {
+    const long long pre = prefix_blocks();
+    long long total = pre;
+    for (int i = 0; i < a.b.n_seqs; ++i) total += seq_blocks(paged_seq(a.b, i), 0) * a.n_kv_heads;
+    if (!take_interval(total, cta, grid)) return false;
+    if (x < pre) {
+      enter_prefix();
+      return true;
+    }
+    long long at = pre;
+    for (int i = 0; i < a.b.n_seqs; ++i) {
+      const long long n = seq_blocks(paged_seq(a.b, i), 0) * a.n_kv_heads;
+      if (x < at + n) {
+        enter_sequence(i, at);
+        return true;
+      }
+      at += n;
+    }
+    return false;
+  }
+
+  // The next piece of the interval (nblk 0 at its end).
+  DG_HD PagedFrag next() {
+    PagedFrag f;
+    f.nblk = 0;
+    if (x >= x1) return f;
+    const int nb = tile_blocks(s, part, tile);
+    f.part = part;
+    f.q0 = s.q0;
+    f.row0 = tile * kRows;
+    f.rows = (int)lmin(kRows, (long long)s.nq * a.G - f.row0);
+    f.kvh = kvh;
+    f.kb0 = (int)lmin(nb - 1, x - tile_x0);
+    f.nblk = (int)lmax(1, lmin(nb - f.kb0, x1 - x));
+    f.limit = tile_limit(s, part, tile);
+    f.vis_max = s.kv;
+    f.vis0 = part == 1 || !a.causal ? s.kv : s.kv - s.nq + 1;
+    f.first = f.kb0 == 0;
+    f.whole = f.first && f.nblk == nb;
+    f.n_cont = (int)((tile_x0 + nb - 1) / per - x / per);
+    f.pages = (int)(((long long)f.limit + (1 << a.b.page_shift) - 1) >> a.b.page_shift);
+    f.page_list = part == 1 ? a.b.prefix_pages : a.b.table + (long long)seq * a.b.table_stride;
+    // step
+    x += f.nblk;
+    if (x < x1 && f.kb0 + f.nblk >= nb) {
+      tile_x0 += nb;
+      if (++tile >= tiles_of(s)) {
+        tile = 0;
+        if (++kvh >= a.n_kv_heads) {
+          kvh = 0;
+          part = 0;
+          do {
+            if (++seq >= a.b.n_seqs) {
+              x = x1;   // (lengths that change while the kernel runs)
+              break;
+            }
+            s = paged_seq(a.b, seq);
+          } while (s.nq == 0);
+        }
+      }
+    }
+    return f;
+  }
+};
+
+// Where a row's piece goes.  meta of a row of a cut tile: {first CTA,
+// later CTAs * kRows + row in the tile}; of a finished row: {-1, 0}.
+struct PagedDest {
+  float* o;       // fp32 destination, or null
+  float* lse;
+  bool final;     // straight to the output
+};
+
+template <int kRows>
+__device__ __forceinline__ PagedDest paged_dest(const PagedAttnArgs& a, const PagedFrag& f, int r, int hd,
+                                                long long row) {
+  PagedDest d;
+  const long long rows = (long long)a.b.n_tokens * a.n_heads;
+  d.final = f.whole && a.b.prefix_len == 0;
+  d.o = nullptr;
+  d.lse = nullptr;
+  if (f.first) a.meta[f.part * rows + row] = d.final ? make_int2(-1, 0)
+                                                     : make_int2((int)blockIdx.x, f.n_cont * kRows + r);
+  if (d.final) return d;
+  if (f.first) {
+    d.o = a.part_o + (f.part * rows + row) * hd;
+    d.lse = a.part_lse + f.part * rows + row;
+  } else {
+    d.o = a.slot_o + ((long long)blockIdx.x * kRows + r) * hd;
+    d.lse = a.slot_lse + (long long)blockIdx.x * kRows + r;
+  }
+  return d;
+}
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Joins the pieces of every row: own keys first, then the prefix, each in key
+// order.  One warp per row; reads what the pieces wrote (mostly from L2).
+template <typename T, int kHd>
+__global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, int grid_main) {
+  pdl_wait();
+  constexpr int kPer = kHd / 32;   // columns a lane
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)a.b.n_tokens * a.n_heads;
+  const int parts = a.b.prefix_len > 0 ? 2 : 1;
+  const int lo = a.b.n_seqs > 0 ? a.b.cu_q[0] : 0, hi = a.b.n_seqs > 0 ? a.b.cu_q[a.b.n_seqs] : 0;
+  for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
+    const int tok = (int)(row / a.n_heads), head = (int)(row % a.n_heads);
+    if (tok < lo || tok >= hi) continue;
+    int2 m[2];
+    m[0] = a.meta[row];
+    m[1] = parts == 2 ? a.meta[rows + row] : make_int2(-1, 0);
+    if (m[0].x < 0) continue;   // written by the main kernel
+    float acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+    float top = -INFINITY, sum = 0.0f;   // reference and sum of 2^(lse - top)
+    auto add = [&](const float* o, float lse) {
+      if (lse == -INFINITY) return;
+      float v[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 u = *reinterpret_cast<const float2*>(o + lane * kPer + i);
+        v[i] = u.x;
+        v[i + 1] = u.y;
+      }
+      const float up = fmaxf(top, lse);
+      const float w0 = top == -INFINITY ? 0.0f : exp2f(top - up), w1 = exp2f(lse - up);
+      top = up;
+      sum = sum * w0 + w1;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * w0 + v[i] * w1;
+    };
+    for (int p = 0; p < parts; ++p) {
+      // (an index from a row no tile covered stays in the workspace)
+      const int c = min(max(m[p].x, 0), grid_main - 1);
+      const int r = m[p].y & (kRows - 1);
+      const int n = min(max(m[p].y / kRows, 0), grid_main - 1 - c);
+      add(a.part_o + (p * rows + row) * kHd, a.part_lse[p * rows + row]);
+      for (int i = 1; i <= n; ++i)
+        add(a.slot_o + ((long long)(c + i) * kRows + r) * kHd, a.slot_lse[(long long)(c + i) * kRows + r]);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    T* dst = (T*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) dst[i] = from_f<T>(acc[i] * inv);
+    if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32: CUDA cores (the tensor cores have no fp32 product).  A CTA of 256
+// threads holds a tile of 64 rows and takes 64 keys at a time; thread (ty, tx)
+// owns the scores of rows 4 ty .. 4 ty + 3 and keys tx + 16 c, and of the
+// output the same rows with the columns 4 tx + 64 c ...
+// ---------------------------------------------------------------------------
+constexpr int kPaF32Rows = 64, kPaF32Blk = 64;
+template <int kHd>
+constexpr int paged_f32_smem() {
+  // Q and K rows padded by 4 floats, V, P rows padded by 4
+  return (kPaF32Rows * (kHd + 4) + kPaF32Blk * (kHd + 4) + kPaF32Blk * kHd + kPaF32Rows * (kPaF32Blk + 4)) * 4;
+}
+
+template <int kHd>
+__global__ void __launch_bounds__(256, 1) k_paged_attn_f32(PagedAttnArgs a) {
+  constexpr int R = kPaF32Rows, B = kPaF32Blk, kLd = kHd + 4, kLdP = B + 4, kOc = kHd / 64;
+  extern __shared__ __align__(16) float sm[];
+  float* sQ = sm;
+  float* sK = sQ + R * kLd;
+  float* sV = sK + B * kLd;
+  float* sP = sV + B * kHd;
+  __shared__ long long s_tmp[256 / 32 + 1];
+  __shared__ int s_found;
+  pdl_enter();
+  PagedWalk<R, B> walk(a);
+  if (!walk.template begin<256>(s_tmp, s_found)) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  for (;;) {
+    const PagedFrag f = walk.next();
+    if (f.nblk == 0) break;
+    __syncthreads();   // the previous piece is done with shared memory
+    for (int i = tid; i < R * (kHd / 4); i += 256) {
+      const int r = i / (kHd / 4), c = i % (kHd / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < f.rows) {
+        const int gr = f.row0 + r;
+        v = *reinterpret_cast<const float4*>((const float*)a.q + (long long)(f.q0 + gr / a.G) * a.q_ts +
+                                             (long long)(f.kvh * a.G + gr % a.G) * a.q_hs + c);
+      }
+      *reinterpret_cast<float4*>(sQ + r * kLd + c) = v;
+    }
+    int vis[4];
+    float top[4], sum[4], o[4][4 * kOc];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int gr = f.row0 + ty * 4 + i;
+      vis[i] = min(f.vis_max, f.vis0 + gr / a.G);
+      top[i] = -INFINITY;
+      sum[i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 4 * kOc; ++c) o[i][c] = 0.0f;
+    }
+    for (int kb = f.kb0; kb < f.kb0 + f.nblk; ++kb) {
+      const int key0 = kb * B;
+      __syncthreads();
+      // keys and values of the block; rows past the last visible key are zero,
+      // so what the cache holds there never enters a sum
+      for (int i = tid; i < B * (kHd / 4); i += 256) {
+        const int r = i / (kHd / 4), c = i % (kHd / 4) * 4, key = key0 + r;
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+        if (key < f.limit) {
+          const int page = f.page_list[key >> a.b.page_shift];
+          if (page >= 0 && page < a.b.n_pages) {
+            const long long off = ((((long long)page * a.n_kv_heads + f.kvh) << a.b.page_shift) +
+                                   (key & ((1 << a.b.page_shift) - 1))) * kHd + c;
+            k = *reinterpret_cast<const float4*>((const float*)a.k_pages + off);
+            v = *reinterpret_cast<const float4*>((const float*)a.v_pages + off);
+          } else {
+            dev_error(a.b.status, kStatusState);
+          }
+        }
+        *reinterpret_cast<float4*>(sK + r * kLd + c) = k;
+        *reinterpret_cast<float4*>(sV + r * kHd + c) = v;
+      }
+      __syncthreads();
+      float s[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 4
+      for (int d = 0; d < kHd; d += 4) {
+        float4 qv[4], kv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty * 4 + i) * kLd + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * kLd + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[i][j] += qv[i].x * kv[j].x + qv[i].y * kv[j].y + qv[i].z * kv[j].z + qv[i].w * kv[j].w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = key0 + tx + 16 * j < vis[i] ? s[i][j] * a.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const float up = fmaxf(top[i], mx);
+        const float old = top[i] == -INFINITY ? 0.0f : exp2f(top[i] - up);
+        float add = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = up == -INFINITY ? 0.0f : exp2f(s[i][j] - up);
+          add += p;
+          sP[(ty * 4 + i) * kLdP + tx + 16 * j] = p;
+        }
+#pragma unroll
+        for (int w = 8; w; w >>= 1) add += __shfl_xor_sync(0xffffffffu, add, w);
+        sum[i] = sum[i] * old + add;
+        top[i] = up;
+#pragma unroll
+        for (int c = 0; c < 4 * kOc; ++c) o[i][c] *= old;
+      }
+      __syncwarp();   // rows 4 ty .. belong to one half warp
+#pragma unroll 2
+      for (int k = 0; k < B; k += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * 4 + i) * kLdP + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+          for (int c = 0; c < kOc; ++c) {
+            const float4 v = *reinterpret_cast<const float4*>(sV + (k + kk) * kHd + c * 64 + tx * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float pp = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+              o[i][c * 4] += pp * v.x;
+              o[i][c * 4 + 1] += pp * v.y;
+              o[i][c * 4 + 2] += pp * v.z;
+              o[i][c * 4 + 3] += pp * v.w;
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      if (r >= f.rows) continue;
+      const int gr = f.row0 + r, tok = f.q0 + gr / a.G, head = f.kvh * a.G + gr % a.G;
+      const long long row = (long long)tok * a.n_heads + head;
+      const float inv = sum[i] > 0.0f ? 1.0f / sum[i] : 0.0f;
+      const float l2 = sum[i] > 0.0f ? top[i] + log2f(sum[i]) : -INFINITY;
+      // (all 16 threads of the row store the same meta)
+      const PagedDest d = paged_dest<R>(a, f, r, kHd, row);
+      float* dst = d.final ? (float*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs : d.o;
+#pragma unroll
+      for (int c = 0; c < kOc; ++c)
+        *reinterpret_cast<float4*>(dst + c * 64 + tx * 4) =
+            make_float4(o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv);
+      if (tx == 0) {
+        if (!d.final) *d.lse = l2;
+        else if (a.lse) a.lse[row] = l2 * kLn2;
+      }
+    }
+  }
+}

@@ -1,0 +1,376 @@
+"""Serving operators over a paged key/value cache (include/dg.h).
+
+Argument checks and marshalling; the work is in libdg.so.  Tensors may be
+views with any token and head stride as long as the components of a head are
+contiguous.  Every call is asynchronous on `stream` (default: the current
+stream of the tensors' device), allocates nothing but a workspace the caller
+did not bring, and can be captured into a CUDA graph.
+
+    cache = PagedKV(k_pages, v_pages)                   # [n_pages, Hkv, page, hd]
+    batch = PagedBatch(cu_q, kv_lens, page_table)       # device int32
+    paged_append(cache, batch, k, v, rope=rope, norm=norm, q=q, q_out=q)
+    paged_attention(cache, batch, q, out)
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+_I32, _I64, _F, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _P), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", _P), ("rot_dim", _I32), ("interleaved", _I32), ("amplitude", _F)]
+
+
+class _HeadNorm(ctypes.Structure):
+    _fields_ = [("enabled", _I32), ("eps", _F), ("q_gain", _P), ("k_gain", _P)]
+
+
+class _PagedKV(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("dtype", _I32), ("n_pages", _I32), ("n_kv_heads", _I32), ("page_size", _I32),
+                ("head_dim", _I32)]
+
+
+class _PagedBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", _I32), ("n_tokens", _I32), ("cu_q", _P), ("kv_lens", _P), ("page_table", _P),
+                ("table_stride", _I64), ("max_pages", _I32), ("prefix_pages", _P), ("prefix_len", _I32)]
+
+
+def signatures():
+    """ctypes signatures of the operators' entry points (see lib())."""
+    H, R, N = ctypes.POINTER(_Heads), ctypes.POINTER(_Rope), ctypes.POINTER(_HeadNorm)
+    KV, B = ctypes.POINTER(_PagedKV), ctypes.POINTER(_PagedBatch)
+    return {
+        "dg_qk_norm_rope": ([_I32, _I32, _I32, _I32, _I32, H, H, H, H, _P, R, N, _P], _I32),
+        "dg_paged_append": ([KV, B, H, H, R, N, _I32, H, H, _P, _P], _I32),
+        "dg_paged_attention_workspace": ([_I32, _I32, _I32, _I32], ctypes.c_size_t),
+        "dg_paged_attention": ([KV, B, _I32, H, _F, _I32, H, _P, _P, ctypes.c_size_t, _P, _P], _I32),
+        "dg_test_paged_walk": ([KV, B, _I32, _I32, _I32, _P, _P, _I32, _P], _I32),
+    }
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name, dtype, dim, device=None, contiguous=False):
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == dim,
+          f"{name} must be a {dim}-D {dtype} tensor")
+    _need(device is None or t.device == device, f"{name} must be on {device}")
+    _need(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+    return t
+
+
+def _head_rows(t, name, dtype, tokens, heads, dim, device):
+    _tensor(t, name, dtype, 3, device)
+    _need(tuple(t.shape) == (tokens, heads, dim), f"{name} must be [{tokens}, {heads}, {dim}], got {list(t.shape)}")
+    st, sh, si = t.stride()
+    _need(si == 1 or dim == 1 or t.numel() == 0, f"{name}: the components of a head must be contiguous")
+    return _Heads(t.data_ptr(), st, sh)
+
+
+def _out_rows(t, name, dtype, tokens, heads, dim, device):
+    h = _head_rows(t, name, dtype, tokens, heads, dim, device)
+    # rows that share memory would be written by several warps at once
+    a, b = sorted([(t.stride(0), tokens), (t.stride(1), heads)])
+    _need(t.numel() == 0 or ((a[1] == 1 or a[0] >= dim) and (b[1] == 1 or b[0] >= (a[1] - 1) * a[0] + dim)),
+          f"{name}: rows overlap")
+    return h
+
+
+def _dtype_code(dtype):
+    import torch
+    _need(dtype in (torch.float32, torch.bfloat16), f"dtype must be float32 or bfloat16, got {dtype}")
+    return 1 if dtype == torch.bfloat16 else 0
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+class Rope:
+    """Position rotation: pair j of a head turns by position * inv_freq[j].
+
+    inv_freq: float64 device tensor [rot_dim / 2] (see rope_frequencies); the
+    first rot_dim components rotate, the rest pass.  interleaved False pairs
+    (j, j + rot_dim / 2), True pairs (2j, 2j + 1).  amplitude multiplies the
+    rotated components (long-context scalings use it)."""
+
+    def __init__(self, inv_freq, interleaved=False, amplitude=1.0):
+        import torch
+        _tensor(inv_freq, "inv_freq", torch.float64, 1, contiguous=True)
+        _need(inv_freq.is_cuda, "inv_freq must be on a GPU")
+        self.inv_freq = inv_freq
+        self.rot_dim = 2 * inv_freq.numel()
+        self._c = _Rope(inv_freq.data_ptr(), self.rot_dim, int(bool(interleaved)), float(amplitude))
+
+
+class HeadNorm:
+    """RMSNorm of each head: x / sqrt(mean(x^2) + eps) * gain (gains [head_dim], None: ones)."""
+
+    def __init__(self, eps=1e-6, q_gain=None, k_gain=None):
+        _need(eps >= 0.0, "eps must not be negative")
+        self.q_gain, self.k_gain = q_gain, k_gain
+        self._c = _HeadNorm(1, float(eps), None if q_gain is None else q_gain.data_ptr(),
+                            None if k_gain is None else k_gain.data_ptr())
+
+    def _check(self, dtype, dim, device):
+        for name in ("q_gain", "k_gain"):
+            g = getattr(self, name)
+            if g is not None:
+                _tensor(g, name, dtype, 1, device, contiguous=True)
+                _need(g.numel() == dim, f"{name} must have {dim} entries")
+
+
+def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=None, beta_fast=32.0,
+                     beta_slow=1.0):
+    """(inv_freq, amplitude): radians per position of the rot_dim / 2 pairs, as
+    a list of floats for torch.tensor(..., dtype=torch.float64), and the
+    multiplier of the rotated components.
+
+    scaling "none":   w_j = theta^(-2j / rot_dim).
+    scaling "linear": w_j / factor (positions interpolated).
+    scaling "ntk":    theta * factor^(rot_dim / (rot_dim - 2)): the slowest pair
+                      stretches by `factor`, the fastest hardly at all.
+    scaling "yarn":   (Peng et al. 2023) pairs that turn more than beta_fast
+                      times over original_len stay, those below beta_slow turns
+                      are interpolated, a ramp between; amplitude
+                      0.1 ln(factor) + 1."""
+    _need(rot_dim >= 2 and rot_dim % 2 == 0, "rot_dim must be even and positive")
+    _need(theta > 0.0 and factor >= 1.0, "theta must be positive and factor at least 1")
+    _need(scaling in ("none", "linear", "ntk", "yarn"), f"unknown scaling {scaling!r}")
+    n = rot_dim // 2
+    if scaling == "ntk":
+        _need(rot_dim > 2, "ntk scaling needs rot_dim > 2")
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    w = [theta ** (-2.0 * j / rot_dim) for j in range(n)]
+    if scaling == "linear":
+        return [x / factor for x in w], 1.0
+    if scaling != "yarn" or factor == 1.0:
+        return w, 1.0
+    _need(original_len is not None and original_len > 0, "yarn scaling needs original_len")
+    _need(theta > 1.0 and beta_fast > beta_slow > 0.0, "yarn scaling needs theta > 1 and beta_fast > beta_slow > 0")
+
+    def pair_of(turns):   # the (fractional) pair that makes this many turns over original_len
+        return rot_dim * math.log(original_len / (turns * 2.0 * math.pi)) / (2.0 * math.log(theta))
+
+    lo = max(math.floor(pair_of(beta_fast)), 0)
+    hi = min(math.ceil(pair_of(beta_slow)), rot_dim - 1)
+    out = []
+    for j, x in enumerate(w):
+        ramp = min(max((j - lo) / max(hi - lo, 1e-3), 0.0), 1.0)   # 0: as it is, 1: interpolated
+        out.append(x * (1.0 - ramp) + x / factor * ramp)
+    return out, 0.1 * math.log(factor) + 1.0
+
+
+class PagedKV:
+    """A paged cache: keys and values [n_pages, n_kv_heads, page_size, head_dim],
+    contiguous, page_size a power of two from 16 to 256."""
+
+    def __init__(self, k, v):
+        import torch
+        _need(isinstance(k, torch.Tensor) and k.is_cuda, "k must be a tensor on a GPU")
+        code = _dtype_code(k.dtype)
+        _tensor(k, "k", k.dtype, 4, contiguous=True)
+        _tensor(v, "v", k.dtype, 4, k.device, contiguous=True)
+        _need(k.shape == v.shape and k.numel() > 0, "k and v must have one shape, not empty")
+        page = k.shape[2]
+        _need(16 <= page <= 256 and page & (page - 1) == 0, "page_size must be a power of two from 16 to 256")
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self._c = _PagedKV(k.data_ptr(), v.data_ptr(), code, self.n_pages, self.n_kv_heads, page, self.head_dim)
+
+    @classmethod
+    def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype, device="cuda"):
+        """A cache of uninitialised pages."""
+        import torch
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
+
+
+class PagedBatch:
+    """A ragged batch over a paged cache: sequence b has the token rows
+    cu_q[b] .. cu_q[b+1] - 1 as its newest tokens and kv_lens[b] tokens of its
+    own in the cache, those included, in the pages page_table[b].  prefix_len
+    tokens in prefix_pages come before every sequence.  All tensors int32 on
+    the GPU, read there at each call (a captured call sees later contents)."""
+
+    def __init__(self, cu_q, kv_lens, page_table, prefix_pages=None, prefix_len=0):
+        import torch
+        i32 = torch.int32
+        _tensor(cu_q, "cu_q", i32, 1, contiguous=True)
+        _need(cu_q.is_cuda and cu_q.numel() >= 1, "cu_q must be on a GPU, with one entry more than sequences")
+        n = cu_q.numel() - 1
+        _tensor(kv_lens, "kv_lens", i32, 1, cu_q.device, contiguous=True)
+        _need(kv_lens.numel() == n, f"kv_lens must have {n} entries")
+        _tensor(page_table, "page_table", i32, 2, cu_q.device)
+        _need(page_table.shape[0] == n, f"page_table must have {n} rows")
+        _need(page_table.stride(1) == 1 or page_table.shape[1] <= 1, "the entries of a page_table row must be contiguous")
+        _need(n <= 1 or page_table.stride(0) >= page_table.shape[1], "page_table rows overlap")
+        _need(prefix_len >= 0, "prefix_len must not be negative")
+        _need(prefix_len == 0 or prefix_pages is not None, "prefix_len without prefix_pages")
+        if prefix_pages is not None:
+            _tensor(prefix_pages, "prefix_pages", i32, 1, cu_q.device, contiguous=True)
+        self.cu_q, self.kv_lens, self.page_table, self.prefix_pages = cu_q, kv_lens, page_table, prefix_pages
+        self.n_seqs, self.prefix_len, self.device = n, int(prefix_len), cu_q.device
+        self._c = _PagedBatch(n, 0, cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
+                              max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
+                              None if prefix_len == 0 else prefix_pages.data_ptr(), int(prefix_len))
+
+    def _for(self, cache, tokens):
+        _need(self.device == cache.device, "the batch and the cache are on different devices")
+        _need(self.prefix_len == 0 or self.prefix_pages.numel() * cache.page_size >= self.prefix_len,
+              "prefix_pages has fewer pages than prefix_len needs")
+        c = _PagedBatch.from_buffer_copy(self._c)
+        c.n_tokens = tokens
+        return c
+
+
+class _On:
+    """The device and stream of a call: the tensors' device becomes the current
+    one for its length."""
+
+    def __init__(self, device, stream):
+        import torch
+        _need(stream is None or stream.device == device, f"stream must be one of {device}")
+        self._guard = torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        import torch
+        self._guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def _status_ptr(status, device):
+    import torch
+    if status is None:
+        return None
+    _tensor(status, "status", torch.int32, 1, device)
+    _need(status.numel() == 1, "status must have one entry")
+    return status.data_ptr()
+
+
+def qk_norm_rope(q, k, positions, q_out, k_out, rope=None, norm=None, stream=None):
+    """RMSNorm of each query and key head and the position rotation, one pass.
+
+    q [T, Hq, hd] -> q_out, k [T, Hkv, hd] -> k_out (a pair may be None;
+    outputs may be the inputs), positions int32 [T] (None without rope)."""
+    import torch
+
+    from . import _check, lib
+    x = q if q is not None else k
+    _need(isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 3, "q or k must be a 3-D tensor on a GPU")
+    code, (tokens, _, dim), dev = _dtype_code(x.dtype), x.shape, x.device
+    rows, heads = [], []
+    for a, b, name in ((q, q_out, "q"), (k, k_out, "k")):
+        _need((a is None) == (b is None), f"{name} and {name}_out go together")
+        if a is None:
+            rows += [None, None]
+            heads.append(0)
+        else:
+            heads.append(a.shape[1])
+            rows += [_head_rows(a, name, x.dtype, tokens, a.shape[1], dim, dev),
+                     _out_rows(b, name + "_out", x.dtype, tokens, a.shape[1], dim, dev)]
+    _need(rope is None or positions is not None, "rope needs positions")
+    if positions is not None:
+        _tensor(positions, "positions", torch.int32, 1, dev, contiguous=True)
+        _need(positions.numel() == tokens, f"positions must have {tokens} entries")
+    _need(rope is None or rope.inv_freq.device == dev, f"inv_freq must be on {dev}")
+    if norm is not None:
+        norm._check(x.dtype, dim, dev)
+    with _On(dev, stream) as s:
+        _check(lib().dg_qk_norm_rope(code, tokens, heads[0], heads[1], dim, *[_ref(r) for r in rows],
+                                     None if positions is None else positions.data_ptr(),
+                                     _ref(rope._c if rope else None), _ref(norm._c if norm else None),
+                                     s.cuda_stream), "dg_qk_norm_rope")
+
+
+def paged_append(cache, batch, k, v, rope=None, norm=None, q=None, q_out=None, status=None, stream=None):
+    """The batch's new tokens into the cache's pages: k [T, Hkv, hd] normalised
+    and rotated at its position, v as it is; with q [T, Hq, hd] the same tokens'
+    queries, normalised and rotated, into q_out (which may be q).
+
+    status: int32 [1] device tensor, zero before; becomes 5 (DG_ERR_STATE) if a
+    token had no valid slot (it is not stored)."""
+    import torch
+
+    from . import _check, lib
+    _need(isinstance(k, torch.Tensor) and k.dim() == 3, "k must be a 3-D tensor")
+    tokens, dim, dev, hk = k.shape[0], cache.head_dim, cache.device, cache.n_kv_heads
+    kr = _head_rows(k, "k", cache.dtype, tokens, hk, dim, dev)
+    vr = _head_rows(v, "v", cache.dtype, tokens, hk, dim, dev)
+    _need((q is None) == (q_out is None), "q and q_out go together")
+    qr = qo = None
+    hq = 0
+    if q is not None:
+        _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a 3-D tensor")
+        hq = q.shape[1]
+        qr = _head_rows(q, "q", cache.dtype, tokens, hq, dim, dev)
+        qo = _out_rows(q_out, "q_out", cache.dtype, tokens, hq, dim, dev)
+    _need(rope is None or rope.inv_freq.device == dev, f"inv_freq must be on {dev}")
+    if norm is not None:
+        norm._check(cache.dtype, dim, dev)
+    b = batch._for(cache, tokens)
+    with _On(dev, stream) as s:
+        _check(lib().dg_paged_append(_ref(cache._c), _ref(b), _ref(kr), _ref(vr), _ref(rope._c if rope else None),
+                                     _ref(norm._c if norm else None), hq, _ref(qr), _ref(qo),
+                                     _status_ptr(status, dev), s.cuda_stream), "dg_paged_append")
+
+
+def paged_attention_workspace(n_tokens, n_heads, head_dim, with_prefix=False):
+    """Bytes of workspace paged_attention needs for that many token rows."""
+    from . import DGError, lib
+    n = int(lib().dg_paged_attention_workspace(n_tokens, n_heads, head_dim, int(bool(with_prefix))))
+    if n == 0:
+        raise DGError(1, "dg_paged_attention_workspace")
+    return n
+
+
+def paged_attention(cache, batch, q, out, scale=None, causal=True, lse=None, workspace=None, status=None,
+                    stream=None):
+    """Attention of q [T, Hq, hd] over the cache into out (which may be q).
+
+    Every query sees the batch's whole prefix and its sequence's own tokens: all
+    of them, or (causal) those up to its own.  scale defaults to 1 / sqrt(hd).
+    lse: float32 [T, Hq], receives ln(sum(exp(scores))).  A query that sees no
+    key gets zeros and -inf.  workspace: uint8 tensor of at least
+    paged_attention_workspace(...) bytes (None: allocated for the call); two
+    calls that may overlap need two.  status: int32 [1], zero before; becomes 5
+    (DG_ERR_STATE) if a page id or length was out of range."""
+    import torch
+
+    from . import _check, lib
+    _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a 3-D tensor")
+    tokens, hq, dim = q.shape
+    dev = cache.device
+    qr = _head_rows(q, "q", cache.dtype, tokens, hq, cache.head_dim, dev)
+    o = _out_rows(out, "out", cache.dtype, tokens, hq, cache.head_dim, dev)
+    _need(hq >= 1 and hq % cache.n_kv_heads == 0, f"{hq} query heads over {cache.n_kv_heads} key heads")
+    if lse is not None:
+        _tensor(lse, "lse", torch.float32, 2, dev, contiguous=True)
+        _need(tuple(lse.shape) == (tokens, hq), f"lse must be [{tokens}, {hq}]")
+    b = batch._for(cache, tokens)
+    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    with _On(dev, stream) as s:
+        if workspace is None:
+            with torch.cuda.stream(s):   # freed memory goes back to this stream's pool
+                workspace = torch.empty(paged_attention_workspace(tokens, hq, dim, batch.prefix_len > 0),
+                                        dtype=torch.uint8, device=dev)
+        else:
+            _tensor(workspace, "workspace", torch.uint8, 1, dev, contiguous=True)
+        _check(lib().dg_paged_attention(_ref(cache._c), _ref(b), hq, _ref(qr), scale, int(bool(causal)), _ref(o),
+                                        None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                                        workspace.numel(), _status_ptr(status, dev), s.cuda_stream),
+               "dg_paged_attention")

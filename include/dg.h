@@ -208,6 +208,116 @@ int32_t dg_kernels_per_step(const dg_model* model, int32_t B, int32_t P);
 dg_status dg_gemm_splitk_noalloc(const void* A, const void* B, float* out, int32_t M, int32_t N, int32_t K,
                                  int32_t k_splits, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators over a paged key/value cache: RMSNorm of query and key
+ * heads with the position rotation, new tokens into the pages, attention over
+ * the pages with a prefix shared by the whole batch.  The method pages have
+ * no counterpart; they serve several canvases, prompts or single tokens side
+ * by side without one padded cache per canvas.
+ *
+ * All three are asynchronous on `stream`, allocate nothing, keep nothing
+ * between calls and may be captured into a CUDA graph (lengths, page tables
+ * and positions are read on the device at each replay).  Calls that overlap
+ * on the GPU need separate outputs and workspaces, nothing else.  Argument
+ * errors are returned at once with nothing enqueued.  Errors found on the
+ * device (a page id or a length out of range, a wait that ran out) are
+ * written, first one wins, into `status_word`, a device int32 that the caller
+ * sets to 0 (NULL: not reported): DG_ERR_STATE or DG_ERR_TIMEOUT.  No call
+ * reads or writes outside the buffers it was given, whatever these arrays hold.
+ *
+ * Strides count elements.  The components of a head are always contiguous.
+ * ------------------------------------------------------------------------- */
+
+/* Rows of heads: element (token, head, i) at data[token * token_stride + head * head_stride + i]. */
+typedef struct dg_heads {
+  void* data;
+  int64_t token_stride, head_stride;
+} dg_heads;
+
+/* Position rotation.  Pair j < rot_dim / 2 of a head turns by the angle
+ * position * inv_freq[j]: (a, b) -> amplitude (a cos - b sin, b cos + a sin).
+ * The angle is formed in 64 bits, so far positions keep their phase. */
+typedef struct dg_rope {
+  const double* inv_freq; /* device fp64 [rot_dim / 2], radians per position            */
+  int32_t rot_dim;        /* leading components that rotate: even, 0 (none) .. head_dim */
+  int32_t interleaved;    /* 0: pairs (j, j + rot_dim / 2); 1: pairs (2j, 2j + 1)       */
+  float amplitude;        /* multiplies the rotated components (1: a plain rotation)    */
+} dg_rope;
+
+/* RMSNorm of each head before the rotation: x / sqrt(mean(x^2) + eps) * gain. */
+typedef struct dg_head_norm {
+  int32_t enabled;
+  float eps;
+  const void* q_gain;     /* device, the call's dtype, [head_dim]; NULL: ones */
+  const void* k_gain;
+} dg_head_norm;
+
+/* The cache: keys and values, device, `dtype`, each [n_pages][n_kv_heads][page_size][head_dim].
+ * page_size is a power of two, 16 .. 256; both pointers 16-byte aligned. */
+typedef struct dg_paged_kv {
+  void *k, *v;
+  int32_t dtype, n_pages, n_kv_heads, page_size, head_dim;
+} dg_paged_kv;
+
+/* A ragged batch.  Sequence b has the rows cu_q[b] .. cu_q[b+1] - 1 of the
+ * token buffers as its newest tokens and kv_lens[b] tokens of its own in the
+ * cache, those newest ones included: token i of its n new ones is its own
+ * token kv_lens[b] - n + i.  Own token j lies in page page_table[b][j / page_size]
+ * at offset j % page_size; entries past the last needed page are not read.
+ * A prefix of prefix_len tokens in the pages prefix_pages precedes every
+ * sequence (position = prefix_len + own token).  Rows outside
+ * cu_q[0] .. cu_q[n_seqs] - 1 are neither read nor written. */
+typedef struct dg_paged_batch {
+  int32_t n_seqs, n_tokens;     /* n_tokens: rows of the token buffers            */
+  const int32_t* cu_q;          /* device [n_seqs + 1], not decreasing            */
+  const int32_t* kv_lens;       /* device [n_seqs]                                */
+  const int32_t* page_table;    /* device [n_seqs][table_stride]                  */
+  int64_t table_stride;
+  int32_t max_pages;            /* entries of a page_table row that may be read   */
+  const int32_t* prefix_pages;  /* device [ceil(prefix_len / page_size)] or NULL  */
+  int32_t prefix_len;           /* 0: no shared prefix                            */
+} dg_paged_batch;
+
+/* RMSNorm and rotation of query and key heads in one pass.  q [n_tokens, n_heads,
+ * head_dim] -> q_out, k [n_tokens, n_kv_heads, head_dim] -> k_out (either pair may
+ * be absent: n_heads or n_kv_heads 0); outputs may be the inputs themselves, but
+ * may not overlap them otherwise.  positions: device int32 [n_tokens], any sign.
+ * rope or norm NULL: that step is left out.  head_dim is even, 2 .. 256.  Computed
+ * in fp32, rounded once. */
+dg_status dg_qk_norm_rope(int32_t dtype, int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                          const dg_heads* q, const dg_heads* q_out, const dg_heads* k, const dg_heads* k_out,
+                          const int32_t* positions, const dg_rope* rope, const dg_head_norm* norm, void* stream);
+
+/* New tokens into the cache: k [n_tokens, n_kv_heads, head_dim] is normalised and
+ * rotated as above at its position and stored, v is stored as it is, each in the
+ * slot the batch gives it.  With q (n_heads > 0) the same tokens' queries are
+ * normalised and rotated into q_out in the same launch.  A token whose slot does
+ * not exist (own token below 0, past max_pages, page id out of range) is not
+ * stored and reported.  Two tokens with one slot: either may win.  head_dim is
+ * even, 2 .. 256. */
+dg_status dg_paged_append(const dg_paged_kv* cache, const dg_paged_batch* batch, const dg_heads* k,
+                          const dg_heads* v, const dg_rope* rope, const dg_head_norm* norm, int32_t n_heads,
+                          const dg_heads* q, const dg_heads* q_out, int32_t* status_word, void* stream);
+
+/* Bytes of workspace dg_paged_attention needs for n_tokens rows of n_heads
+ * heads, with or without a shared prefix; 0 if an argument is out of range. */
+size_t dg_paged_attention_workspace(int32_t n_tokens, int32_t n_heads, int32_t head_dim, int32_t with_prefix);
+
+/* Attention of q [n_tokens, n_heads, head_dim] over the cache: query head h uses
+ * key head h / (n_heads / n_kv_heads); scores are scale * q.k.  Every query sees
+ * the whole prefix; of its sequence's own tokens it sees all (causal 0) or those
+ * up to its own (causal 1).  out = softmax(scores) V; lse (fp32 [n_tokens,
+ * n_heads], or NULL) = ln(sum(exp(scores))).  A query that sees no key gets zeros
+ * and lse = -inf.  The prefix is read once for the whole batch, not once for
+ * each sequence.  head_dim 64 or 128; q and out 16-byte aligned with strides of a
+ * multiple of 16 bytes; scale > 0; n_heads a multiple of the cache's n_kv_heads.
+ * Memory in the cache past a sequence's length may hold anything; keys and values
+ * within it must be finite.  workspace: device, 256-byte aligned, contents
+ * arbitrary, not shared with a call that may overlap this one.  `out` may be q. */
+dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged_batch* batch, int32_t n_heads,
+                             const dg_heads* q, float scale, int32_t causal, const dg_heads* out, float* lse,
+                             void* workspace, size_t workspace_bytes, int32_t* status_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -241,6 +241,20 @@ dg_status dg_test_moe(dg_model* model, int32_t B, int32_t layer, const void* h_a
 /* Kernel launches recorded in one captured block-loop round (graph body). */
 int32_t dg_launches_per_round(const dg_model* model);
 
+/* Host only: the pieces of work dg_paged_attention cuts a batch into.  Every
+ * pointer of `batch` is host memory here (the cache's pages are not touched).
+ * tile_rows: 256 (bf16 tiles, 128 keys a block) or 64 (fp32 tiles, 64 keys a
+ * block).  out: int32 [cap][16] rows of {CTA, part (0 own keys, 1 the prefix),
+ * sequence (-1: the prefix), first token, first row, rows, key head, first key
+ * block, key blocks, visible keys of the last row, vis0, vis_max (row r sees
+ * the keys below min(vis_max, vis0 + (first row + r) / G)), page list entries,
+ * starts its tile, is its whole tile, later CTAs of the tile}, in CTA order;
+ * *n_out their number.  DG_ERR_INVALID_ARG for bad arguments or more than
+ * `cap` pieces.  status_word (host) as in dg_paged_attention. */
+dg_status dg_test_paged_walk(const dg_paged_kv* cache, const dg_paged_batch* batch, int32_t n_heads,
+                             int32_t causal, int32_t tile_rows, int32_t* status_word, int32_t* out, int32_t cap,
+                             int32_t* n_out);
+
 #ifdef __cplusplus
 }
 #endif
