@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from array import array
 
 _I32, _I64, _F, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -42,16 +43,42 @@ class _PagedBatch(ctypes.Structure):
 
 
 def signatures():
-    """ctypes signatures of the operators' entry points (see lib())."""
-    H, R, N = ctypes.POINTER(_Heads), ctypes.POINTER(_Rope), ctypes.POINTER(_HeadNorm)
-    KV, B = ctypes.POINTER(_PagedKV), ctypes.POINTER(_PagedBatch)
+    """ctypes signatures of the operators' entry points (see lib()); struct
+    arguments go as addresses."""
     return {
-        "dg_qk_norm_rope": ([_I32, _I32, _I32, _I32, _I32, H, H, H, H, _P, R, N, _P], _I32),
-        "dg_paged_append": ([KV, B, H, H, R, N, _I32, H, H, _P, _P], _I32),
+        "dg_qk_norm_rope": ([_I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+        "dg_paged_append": ([_P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _P], _I32),
         "dg_paged_attention_workspace": ([_I32, _I32, _I32, _I32], ctypes.c_size_t),
-        "dg_paged_attention": ([KV, B, _I32, H, _F, _I32, H, _P, _P, ctypes.c_size_t, _P, _P], _I32),
-        "dg_test_paged_walk": ([KV, B, _I32, _I32, _I32, _P, _P, _I32, _P], _I32),
+        "dg_paged_attention": ([_P, _P, _I32, _P, _F, _I32, _P, _P, _P, ctypes.c_size_t, _P, _P], _I32),
+        "dg_test_paged_walk": ([_P, _P, _I32, _I32, _I32, _P, _P, _I32, _P], _I32),
     }
+
+
+class _Runtime:
+    """What every call needs, looked up once: a small call takes the GPU a few
+    microseconds, less than the imports and objects of a careless one."""
+
+    def __init__(self):
+        import torch
+
+        import block_text_diffusion_b200 as package
+        lib = package.lib()
+        self.torch, self.DGError, self.check = torch, package.DGError, package._check
+        self.Tensor, self.f32, self.bf16, self.i32 = torch.Tensor, torch.float32, torch.bfloat16, torch.int32
+        self.norm_rope, self.append = lib.dg_qk_norm_rope, lib.dg_paged_append
+        self.attention, self.workspace = lib.dg_paged_attention, lib.dg_paged_attention_workspace
+        self.current_device = torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_runtime = None
+
+
+def _rt():
+    global _runtime
+    if _runtime is None:
+        _runtime = _Runtime()
+    return _runtime
 
 
 def _need(ok, what):
@@ -61,38 +88,41 @@ def _need(ok, what):
 
 def _tensor(t, name, dtype, dim, device=None, contiguous=False):
     import torch
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() == dim,
-          f"{name} must be a {dim}-D {dtype} tensor")
-    _need(device is None or t.device == device, f"{name} must be on {device}")
-    _need(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
+        raise ValueError(f"{name} must be a {dim}-D {dtype} tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t
 
 
-def _head_rows(t, name, dtype, tokens, heads, dim, device):
-    _tensor(t, name, dtype, 3, device)
-    _need(tuple(t.shape) == (tokens, heads, dim), f"{name} must be [{tokens}, {heads}, {dim}], got {list(t.shape)}")
+def _rows(rt, t, name, dtype, shape, index):
+    """(address, token stride, head stride) of a [tokens, heads, head_dim] tensor."""
+    if not isinstance(t, rt.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on cuda:{index}")
     st, sh, si = t.stride()
-    _need(si == 1 or dim == 1 or t.numel() == 0, f"{name}: the components of a head must be contiguous")
-    return _Heads(t.data_ptr(), st, sh)
+    if si != 1 and shape[2] > 1 and shape[0] * shape[1] > 0:
+        raise ValueError(f"{name}: the components of a head must be contiguous")
+    return t.data_ptr(), st, sh
 
 
-def _out_rows(t, name, dtype, tokens, heads, dim, device):
-    h = _head_rows(t, name, dtype, tokens, heads, dim, device)
-    # rows that share memory would be written by several warps at once
-    a, b = sorted([(t.stride(0), tokens), (t.stride(1), heads)])
-    _need(t.numel() == 0 or ((a[1] == 1 or a[0] >= dim) and (b[1] == 1 or b[0] >= (a[1] - 1) * a[0] + dim)),
-          f"{name}: rows overlap")
-    return h
+def _out_rows(rt, t, name, dtype, shape, index):
+    """The same for an output, whose rows may not share memory (several warps
+    would write them at once)."""
+    r = _rows(rt, t, name, dtype, shape, index)
+    tokens, heads, dim = shape
+    if not (r[2] >= dim and r[1] >= (heads - 1) * r[2] + dim):
+        (a, na), (b, nb) = sorted([(r[1], tokens), (r[2], heads)])
+        if tokens * heads and ((na > 1 and a < dim) or (nb > 1 and b < (na - 1) * a + dim)):
+            raise ValueError(f"{name}: rows overlap")
+    return r
 
 
 def _dtype_code(dtype):
     import torch
     _need(dtype in (torch.float32, torch.bfloat16), f"dtype must be float32 or bfloat16, got {dtype}")
     return 1 if dtype == torch.bfloat16 else 0
-
-
-def _ref(s):
-    return None if s is None else ctypes.byref(s)
 
 
 class Rope:
@@ -107,9 +137,10 @@ class Rope:
         import torch
         _tensor(inv_freq, "inv_freq", torch.float64, 1, contiguous=True)
         _need(inv_freq.is_cuda, "inv_freq must be on a GPU")
-        self.inv_freq = inv_freq
+        self.inv_freq, self.index = inv_freq, inv_freq.get_device()
         self.rot_dim = 2 * inv_freq.numel()
         self._c = _Rope(inv_freq.data_ptr(), self.rot_dim, int(bool(interleaved)), float(amplitude))
+        self._at = ctypes.addressof(self._c)
 
 
 class HeadNorm:
@@ -120,13 +151,13 @@ class HeadNorm:
         self.q_gain, self.k_gain = q_gain, k_gain
         self._c = _HeadNorm(1, float(eps), None if q_gain is None else q_gain.data_ptr(),
                             None if k_gain is None else k_gain.data_ptr())
+        self._at = ctypes.addressof(self._c)
 
-    def _check(self, dtype, dim, device):
-        for name in ("q_gain", "k_gain"):
-            g = getattr(self, name)
-            if g is not None:
-                _tensor(g, name, dtype, 1, device, contiguous=True)
-                _need(g.numel() == dim, f"{name} must have {dim} entries")
+    def _check(self, rt, dtype, dim, index):
+        for g in (self.q_gain, self.k_gain):
+            if g is not None and (g.dtype is not dtype or g.shape != (dim,) or g.get_device() != index
+                                  or not g.is_contiguous()):
+                raise ValueError(f"gains must be contiguous {dtype} tensors of {dim} entries on cuda:{index}")
 
 
 def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=None, beta_fast=32.0,
@@ -183,9 +214,10 @@ class PagedKV:
         _need(k.shape == v.shape and k.numel() > 0, "k and v must have one shape, not empty")
         page = k.shape[2]
         _need(16 <= page <= 256 and page & (page - 1) == 0, "page_size must be a power of two from 16 to 256")
-        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.device
+        self.k, self.v, self.dtype, self.device, self.index = k, v, k.dtype, k.device, k.get_device()
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self._c = _PagedKV(k.data_ptr(), v.data_ptr(), code, self.n_pages, self.n_kv_heads, page, self.head_dim)
+        self._at = ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype, device="cuda"):
@@ -214,52 +246,45 @@ class PagedBatch:
         _need(page_table.shape[0] == n, f"page_table must have {n} rows")
         _need(page_table.stride(1) == 1 or page_table.shape[1] <= 1, "the entries of a page_table row must be contiguous")
         _need(n <= 1 or page_table.stride(0) >= page_table.shape[1], "page_table rows overlap")
-        _need(prefix_len >= 0, "prefix_len must not be negative")
+        _need(0 <= prefix_len < 1 << 31, "prefix_len must lie in [0, 2^31)")
         _need(prefix_len == 0 or prefix_pages is not None, "prefix_len without prefix_pages")
         if prefix_pages is not None:
             _tensor(prefix_pages, "prefix_pages", i32, 1, cu_q.device, contiguous=True)
         self.cu_q, self.kv_lens, self.page_table, self.prefix_pages = cu_q, kv_lens, page_table, prefix_pages
-        self.n_seqs, self.prefix_len, self.device = n, int(prefix_len), cu_q.device
-        self._c = _PagedBatch(n, 0, cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
-                              max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
-                              None if prefix_len == 0 else prefix_pages.data_ptr(), int(prefix_len))
+        self.n_seqs, self.prefix_len, self.index = n, int(prefix_len), cu_q.get_device()
+        # dg_paged_batch as 8-byte words, behind the first (n_seqs, n_tokens)
+        self._words = (cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
+                       max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
+                       prefix_pages.data_ptr() if prefix_len else 0, int(prefix_len))
 
-    def _for(self, cache, tokens):
-        _need(self.device == cache.device, "the batch and the cache are on different devices")
-        _need(self.prefix_len == 0 or self.prefix_pages.numel() * cache.page_size >= self.prefix_len,
-              "prefix_pages has fewer pages than prefix_len needs")
-        c = _PagedBatch.from_buffer_copy(self._c)
-        c.n_tokens = tokens
-        return c
-
-
-class _On:
-    """The device and stream of a call: the tensors' device becomes the current
-    one for its length."""
-
-    def __init__(self, device, stream):
-        import torch
-        _need(stream is None or stream.device == device, f"stream must be one of {device}")
-        self._guard = torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        import torch
-        self._guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return s
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
+    def _check(self, cache):
+        if self.index != cache.index:
+            raise ValueError("the batch and the cache are on different devices")
+        if self.prefix_len and self.prefix_pages.numel() * cache.page_size < self.prefix_len:
+            raise ValueError("prefix_pages has fewer pages than prefix_len needs")
 
 
-def _status_ptr(status, device):
-    import torch
+def _launch(rt, index, stream, name, call):
+    """call(stream handle) with the tensors' device current."""
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream must be one of cuda:{index}")
+    if rt.current_device() == index:
+        rt.check(call(rt.raw_stream(index) if stream is None else stream.cuda_stream), name)
+    else:
+        with rt.torch.cuda.device(index):
+            rt.check(call(rt.raw_stream(index) if stream is None else stream.cuda_stream), name)
+
+
+def _status_at(rt, status, index):
     if status is None:
         return None
-    _tensor(status, "status", torch.int32, 1, device)
-    _need(status.numel() == 1, "status must have one entry")
+    if not isinstance(status, rt.Tensor) or status.dtype is not rt.i32 or status.shape != (1,) \
+            or status.get_device() != index:
+        raise ValueError(f"status must be an int32 tensor of one entry on cuda:{index}")
     return status.data_ptr()
+
+
+_NO_ROWS = (0, 0, 0)
 
 
 def qk_norm_rope(q, k, positions, q_out, k_out, rope=None, norm=None, stream=None):
@@ -267,34 +292,42 @@ def qk_norm_rope(q, k, positions, q_out, k_out, rope=None, norm=None, stream=Non
 
     q [T, Hq, hd] -> q_out, k [T, Hkv, hd] -> k_out (a pair may be None;
     outputs may be the inputs), positions int32 [T] (None without rope)."""
-    import torch
-
-    from . import _check, lib
+    rt = _rt()
     x = q if q is not None else k
-    _need(isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 3, "q or k must be a 3-D tensor on a GPU")
-    code, (tokens, _, dim), dev = _dtype_code(x.dtype), x.shape, x.device
-    rows, heads = [], []
-    for a, b, name in ((q, q_out, "q"), (k, k_out, "k")):
-        _need((a is None) == (b is None), f"{name} and {name}_out go together")
-        if a is None:
-            rows += [None, None]
-            heads.append(0)
-        else:
-            heads.append(a.shape[1])
-            rows += [_head_rows(a, name, x.dtype, tokens, a.shape[1], dim, dev),
-                     _out_rows(b, name + "_out", x.dtype, tokens, a.shape[1], dim, dev)]
-    _need(rope is None or positions is not None, "rope needs positions")
+    if not isinstance(x, rt.Tensor) or not x.is_cuda or x.dim() != 3:
+        raise ValueError("q or k must be a 3-D tensor on a GPU")
+    dtype, (tokens, _, dim), index = x.dtype, x.shape, x.get_device()
+    code = 1 if dtype is rt.bf16 else _dtype_code(dtype)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out, k and k_out go together")
+    hq = hk = 0
+    qr = qo = kr = ko = _NO_ROWS
+    if q is not None:
+        hq = q.shape[1]
+        shape = (tokens, hq, dim)
+        qr, qo = _rows(rt, q, "q", dtype, shape, index), _out_rows(rt, q_out, "q_out", dtype, shape, index)
+    if k is not None:
+        hk = k.shape[1] if k.dim() == 3 else 0
+        shape = (tokens, hk, dim)
+        kr, ko = _rows(rt, k, "k", dtype, shape, index), _out_rows(rt, k_out, "k_out", dtype, shape, index)
+    at = None
     if positions is not None:
-        _tensor(positions, "positions", torch.int32, 1, dev, contiguous=True)
-        _need(positions.numel() == tokens, f"positions must have {tokens} entries")
-    _need(rope is None or rope.inv_freq.device == dev, f"inv_freq must be on {dev}")
+        if not isinstance(positions, rt.Tensor) or positions.dtype is not rt.i32 or positions.shape != (tokens,) \
+                or positions.get_device() != index or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 tensor of {tokens} entries on cuda:{index}")
+        at = positions.data_ptr()
+    if rope is not None:
+        if at is None:
+            raise ValueError("rope needs positions")
+        if rope.index != index:
+            raise ValueError(f"inv_freq must be on cuda:{index}")
     if norm is not None:
-        norm._check(x.dtype, dim, dev)
-    with _On(dev, stream) as s:
-        _check(lib().dg_qk_norm_rope(code, tokens, heads[0], heads[1], dim, *[_ref(r) for r in rows],
-                                     None if positions is None else positions.data_ptr(),
-                                     _ref(rope._c if rope else None), _ref(norm._c if norm else None),
-                                     s.cuda_stream), "dg_qk_norm_rope")
+        norm._check(rt, dtype, dim, index)
+    args = array("q", (*qr, *qo, *kr, *ko))
+    p = args.buffer_info()[0]
+    _launch(rt, index, stream, "dg_qk_norm_rope", lambda s: rt.norm_rope(
+        code, tokens, hq, hk, dim, p, p + 24, p + 48, p + 72, at, None if rope is None else rope._at,
+        None if norm is None else norm._at, s))
 
 
 def paged_append(cache, batch, k, v, rope=None, norm=None, q=None, q_out=None, status=None, stream=None):
@@ -304,37 +337,36 @@ def paged_append(cache, batch, k, v, rope=None, norm=None, q=None, q_out=None, s
 
     status: int32 [1] device tensor, zero before; becomes 5 (DG_ERR_STATE) if a
     token had no valid slot (it is not stored)."""
-    import torch
-
-    from . import _check, lib
-    _need(isinstance(k, torch.Tensor) and k.dim() == 3, "k must be a 3-D tensor")
-    tokens, dim, dev, hk = k.shape[0], cache.head_dim, cache.device, cache.n_kv_heads
-    kr = _head_rows(k, "k", cache.dtype, tokens, hk, dim, dev)
-    vr = _head_rows(v, "v", cache.dtype, tokens, hk, dim, dev)
-    _need((q is None) == (q_out is None), "q and q_out go together")
-    qr = qo = None
-    hq = 0
+    rt = _rt()
+    if not isinstance(k, rt.Tensor) or k.dim() != 3 or (q is None) != (q_out is None):
+        raise ValueError("k must be a 3-D tensor, and q and q_out go together")
+    dtype, index, dim, tokens = cache.dtype, cache.index, cache.head_dim, k.shape[0]
+    shape = (tokens, cache.n_kv_heads, dim)
+    kr, vr = _rows(rt, k, "k", dtype, shape, index), _rows(rt, v, "v", dtype, shape, index)
+    hq, qr, qo = 0, _NO_ROWS, _NO_ROWS
     if q is not None:
-        _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a 3-D tensor")
-        hq = q.shape[1]
-        qr = _head_rows(q, "q", cache.dtype, tokens, hq, dim, dev)
-        qo = _out_rows(q_out, "q_out", cache.dtype, tokens, hq, dim, dev)
-    _need(rope is None or rope.inv_freq.device == dev, f"inv_freq must be on {dev}")
+        hq = q.shape[1] if q.dim() == 3 else 0
+        shape = (tokens, hq, dim)
+        qr, qo = _rows(rt, q, "q", dtype, shape, index), _out_rows(rt, q_out, "q_out", dtype, shape, index)
+    if rope is not None and rope.index != index:
+        raise ValueError(f"inv_freq must be on cuda:{index}")
     if norm is not None:
-        norm._check(cache.dtype, dim, dev)
-    b = batch._for(cache, tokens)
-    with _On(dev, stream) as s:
-        _check(lib().dg_paged_append(_ref(cache._c), _ref(b), _ref(kr), _ref(vr), _ref(rope._c if rope else None),
-                                     _ref(norm._c if norm else None), hq, _ref(qr), _ref(qo),
-                                     _status_ptr(status, dev), s.cuda_stream), "dg_paged_append")
+        norm._check(rt, dtype, dim, index)
+    batch._check(cache)
+    args = array("q", (*kr, *vr, *qr, *qo, batch.n_seqs | tokens << 32, *batch._words))
+    p = args.buffer_info()[0]
+    word = _status_at(rt, status, index)
+    _launch(rt, index, stream, "dg_paged_append", lambda s: rt.append(
+        cache._at, p + 96, p, p + 24, None if rope is None else rope._at, None if norm is None else norm._at, hq,
+        p + 48, p + 72, word, s))
 
 
 def paged_attention_workspace(n_tokens, n_heads, head_dim, with_prefix=False):
     """Bytes of workspace paged_attention needs for that many token rows."""
-    from . import DGError, lib
-    n = int(lib().dg_paged_attention_workspace(n_tokens, n_heads, head_dim, int(bool(with_prefix))))
+    rt = _rt()
+    n = int(rt.workspace(n_tokens, n_heads, head_dim, int(bool(with_prefix))))
     if n == 0:
-        raise DGError(1, "dg_paged_attention_workspace")
+        raise rt.DGError(1, "dg_paged_attention_workspace")
     return n
 
 
@@ -349,28 +381,34 @@ def paged_attention(cache, batch, q, out, scale=None, causal=True, lse=None, wor
     paged_attention_workspace(...) bytes (None: allocated for the call); two
     calls that may overlap need two.  status: int32 [1], zero before; becomes 5
     (DG_ERR_STATE) if a page id or length was out of range."""
-    import torch
-
-    from . import _check, lib
-    _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a 3-D tensor")
-    tokens, hq, dim = q.shape
-    dev = cache.device
-    qr = _head_rows(q, "q", cache.dtype, tokens, hq, cache.head_dim, dev)
-    o = _out_rows(out, "out", cache.dtype, tokens, hq, cache.head_dim, dev)
-    _need(hq >= 1 and hq % cache.n_kv_heads == 0, f"{hq} query heads over {cache.n_kv_heads} key heads")
+    rt = _rt()
+    if not isinstance(q, rt.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a 3-D tensor")
+    tokens, hq, _ = q.shape
+    dtype, index, dim = cache.dtype, cache.index, cache.head_dim
+    shape = (tokens, hq, dim)
+    qr, o = _rows(rt, q, "q", dtype, shape, index), _out_rows(rt, out, "out", dtype, shape, index)
+    if hq < 1 or hq % cache.n_kv_heads:
+        raise ValueError(f"{hq} query heads over {cache.n_kv_heads} key heads")
+    lse_at = None
     if lse is not None:
-        _tensor(lse, "lse", torch.float32, 2, dev, contiguous=True)
-        _need(tuple(lse.shape) == (tokens, hq), f"lse must be [{tokens}, {hq}]")
-    b = batch._for(cache, tokens)
-    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
-    with _On(dev, stream) as s:
-        if workspace is None:
-            with torch.cuda.stream(s):   # freed memory goes back to this stream's pool
-                workspace = torch.empty(paged_attention_workspace(tokens, hq, dim, batch.prefix_len > 0),
-                                        dtype=torch.uint8, device=dev)
-        else:
-            _tensor(workspace, "workspace", torch.uint8, 1, dev, contiguous=True)
-        _check(lib().dg_paged_attention(_ref(cache._c), _ref(b), hq, _ref(qr), scale, int(bool(causal)), _ref(o),
-                                        None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                        workspace.numel(), _status_ptr(status, dev), s.cuda_stream),
-               "dg_paged_attention")
+        if not isinstance(lse, rt.Tensor) or lse.dtype is not rt.f32 or lse.shape != (tokens, hq) \
+                or lse.get_device() != index or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor [{tokens}, {hq}] on cuda:{index}")
+        lse_at = lse.data_ptr()
+    batch._check(cache)
+    if workspace is None:
+        s = stream if stream is not None else rt.torch.cuda.current_stream(index)
+        with rt.torch.cuda.stream(s):   # freed, the memory goes back to this stream's pool
+            workspace = rt.torch.empty(paged_attention_workspace(tokens, hq, dim, batch.prefix_len > 0),
+                                       dtype=rt.torch.uint8, device=cache.device)
+    elif not isinstance(workspace, rt.Tensor) or workspace.dtype is not rt.torch.uint8 or workspace.dim() != 1 \
+            or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous 1-D uint8 tensor on cuda:{index}")
+    args = array("q", (*qr, *o, batch.n_seqs | tokens << 32, *batch._words))
+    p = args.buffer_info()[0]
+    word = _status_at(rt, status, index)
+    scale = dim ** -0.5 if scale is None else scale
+    _launch(rt, index, stream, "dg_paged_attention", lambda s: rt.attention(
+        cache._at, p + 48, hq, p, scale, 1 if causal else 0, p + 24, lse_at, workspace.data_ptr(),
+        workspace.numel(), word, s))
