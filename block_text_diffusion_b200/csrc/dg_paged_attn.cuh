@@ -13,7 +13,8 @@
 // Work.  For one key head, the rows (token, query head of the group) of a
 // sequence are cut into tiles of kRows rows, and each tile has the key blocks
 // its rows can see.  All (part, sequence, key head, tile, key block) units lie
-// on one line; CTA c takes the c-th of equal intervals of it.  A CTA so gets
+// on one line, every tile preceded by kTileCost units for what a tile costs
+// besides its blocks; CTA c takes the c-th of equal intervals of it.  A CTA so gets
 // the end of one tile, whole tiles, and the start of another, whatever the
 // lengths are, and no length has to be known on the host.  A tile that lies in
 // one interval goes straight to the output; of a cut tile the CTA holding its
@@ -22,12 +23,28 @@
 #pragma once
 #include "dg_paged.cuh"
 
+// n / d for n < 65536 and 1 <= d <= 32768 by one multiplication: with
+// m = ceil(2^32 / d), m d - 2^32 < d, so n (m d - 2^32) < 2^32 and
+// floor(n m / 2^32) = floor(n / d).  (d = 1: m would be 2^32.)
+struct SmallDiv {
+  uint32_t m;
+  static uint32_t magic(uint32_t d) { return d == 1 ? 0u : (uint32_t)(((1ull << 32) + d - 1) / d); }
+  DG_HD int div(int n) const {
+#ifdef __CUDA_ARCH__
+    return m ? (int)__umulhi((uint32_t)n, m) : n;
+#else
+    return m ? (int)(((uint64_t)(uint32_t)n * m) >> 32) : n;
+#endif
+  }
+};
+
 struct PagedAttnArgs {
   PagedBatch b;
   const void* q;
   void* out;
   long long q_ts, q_hs, o_ts, o_hs;   // token and head strides, elements
   int n_heads, n_kv_heads, G;         // G = n_heads / n_kv_heads
+  SmallDiv by_g;
   int causal;
   float scale_log2;                   // scale * log2(e)
   const void *k_pages, *v_pages;
@@ -46,6 +63,7 @@ struct PagedFrag {
   int part;        // 0: own keys, 1: the prefix
   int q0;          // first token of the sequence (part 1: of the batch)
   int row0, rows;  // the tile's first row of the sequence (row = token * G + head in group), its rows
+  int tok0, rem0;  // row0 / G, row0 % G: row r of the tile is token tok0 + (rem0 + r) / G
   int kvh;         // key head
   int kb0;
   int limit;       // keys the tile's last row can see
@@ -57,6 +75,10 @@ struct PagedFrag {
   int n_cont;      // later CTAs that hold pieces of this tile (valid where first)
   const int* page_list;
 };
+
+// Starting and ending a tile (query rows in, first scores, output) takes about
+// as long as two key blocks, measured on both kernels.
+constexpr int kTileCost = 2;
 
 template <int kRows, int kBlk>
 struct PagedWalk {
@@ -81,12 +103,12 @@ struct PagedWalk {
   DG_HD int tile_blocks(const PagedSeq& q, int part_, int tl) const {
     return imax(1, (int)(((long long)tile_limit(q, part_, tl) + kBlk - 1) / kBlk));
   }
-  // key blocks of all tiles of one sequence for one key head
-  DG_HD long long seq_blocks(const PagedSeq& q, int part_) const {
+  // units of all tiles of one sequence for one key head
+  DG_HD long long seq_units(const PagedSeq& q, int part_) const {
     const int n = tiles_of(q);
-    if (part_ == 1 || !a.causal) return (long long)n * tile_blocks(q, part_, 0);
+    if (part_ == 1 || !a.causal) return (long long)n * (kTileCost + tile_blocks(q, part_, 0));
     long long sum = 0;
-    for (int i = 0; i < n; ++i) sum += tile_blocks(q, part_, i);
+    for (int i = 0; i < n; ++i) sum += kTileCost + tile_blocks(q, part_, i);
     return sum;
   }
   DG_HD PagedSeq whole_batch() const {
@@ -98,10 +120,10 @@ struct PagedWalk {
     p.kv = b.prefix_len;
     return p;
   }
-  DG_HD long long prefix_blocks() const {
-    return a.b.prefix_len > 0 ? seq_blocks(whole_batch(), 1) * a.n_kv_heads : 0;
+  DG_HD long long prefix_units() const {
+    return a.b.prefix_len > 0 ? seq_units(whole_batch(), 1) * a.n_kv_heads : 0;
   }
-  // Interval `cta` of `grid` equal ones of a line of `total` blocks; false if it is empty.
+  // Interval `cta` of `grid` equal ones of a line of `total` units; false if it is empty.
   DG_HD bool take_interval(long long total, int cta, int grid) {
     per = lmax(1, (total + grid - 1) / grid);
     x = lmin(total, cta * per);
@@ -112,22 +134,22 @@ struct PagedWalk {
     part = 1;
     seq = -1;
     s = whole_batch();
-    const long long each = seq_blocks(s, 1), nb = tile_blocks(s, 1, 0);
+    const long long each = seq_units(s, 1), len = kTileCost + tile_blocks(s, 1, 0);
     kvh = (int)(x / each);
-    tile = (int)(x % each / nb);
-    tile_x0 = kvh * each + tile * nb;
+    tile = (int)(x % each / len);
+    tile_x0 = kvh * each + tile * len;
   }
   // x lies in sequence i, which starts at x0 on the line
   DG_HD void enter_sequence(int i, long long x0) {
     part = 0;
     seq = i;
     s = paged_seq(a.b, i);
-    const long long each = lmax(1, seq_blocks(s, 0));
+    const long long each = lmax(1, seq_units(s, 0));
     kvh = (int)lmin(a.n_kv_heads - 1, (x - x0) / each);
     tile = 0;
     tile_x0 = x0 + kvh * each;
     const int n = tiles_of(s);
-    for (int nb; tile + 1 < n && x >= tile_x0 + (nb = tile_blocks(s, 0, tile)); ++tile) tile_x0 += nb;
+    for (int len; tile + 1 < n && x >= tile_x0 + (len = kTileCost + tile_blocks(s, 0, tile)); ++tile) tile_x0 += len;
   }
 
   // Finds the CTA's interval and where it starts; called by all kThreads
@@ -138,10 +160,11 @@ struct PagedWalk {
   __device__ bool begin(long long (&tmp)[kThreads / 32 + 1], int& found) {
     const PagedBatch& b = a.b;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long pre = prefix_units();
     const int run = (b.n_seqs + kThreads - 1) / kThreads;
     const int i0 = min(b.n_seqs, (int)threadIdx.x * run), i1 = min(b.n_seqs, i0 + run);
     long long sum = 0;
-    for (int i = i0; i < i1; ++i) sum += seq_blocks(paged_seq(b, i), 0);
+    for (int i = i0; i < i1; ++i) sum += seq_units(paged_seq(b, i), 0);
     sum *= a.n_kv_heads;
     long long incl = sum;
 #pragma unroll
@@ -158,7 +181,6 @@ struct PagedWalk {
       total += tmp[i];
     }
     incl += before;
-    const long long pre = prefix_blocks();
     if (!take_interval(total + pre, blockIdx.x, gridDim.x)) return false;
     if (x < pre) {
       enter_prefix();
@@ -169,7 +191,7 @@ struct PagedWalk {
     if (y >= incl - sum && y < incl) {
       long long at = incl - sum;
       for (int i = i0; i < i1; ++i) {
-        const long long n = seq_blocks(paged_seq(b, i), 0) * a.n_kv_heads;
+        const long long n = seq_units(paged_seq(b, i), 0) * a.n_kv_heads;
         if (y < at + n) {
           found = i;
           tmp[kThreads / 32] = pre + at;
@@ -186,9 +208,9 @@ struct PagedWalk {
 
   // The same on the host, for a batch in host memory.
   bool begin_host(int cta, int grid) {
-    const long long pre = prefix_blocks();
+    const long long pre = prefix_units();
     long long total = pre;
-    for (int i = 0; i < a.b.n_seqs; ++i) total += seq_blocks(paged_seq(a.b, i), 0) * a.n_kv_heads;
+    for (int i = 0; i < a.b.n_seqs; ++i) total += seq_units(paged_seq(a.b, i), 0) * a.n_kv_heads;
     if (!take_interval(total, cta, grid)) return false;
     if (x < pre) {
       enter_prefix();
@@ -196,7 +218,7 @@ struct PagedWalk {
     }
     long long at = pre;
     for (int i = 0; i < a.b.n_seqs; ++i) {
-      const long long n = seq_blocks(paged_seq(a.b, i), 0) * a.n_kv_heads;
+      const long long n = seq_units(paged_seq(a.b, i), 0) * a.n_kv_heads;
       if (x < at + n) {
         enter_sequence(i, at);
         return true;
@@ -210,41 +232,49 @@ struct PagedWalk {
   DG_HD PagedFrag next() {
     PagedFrag f;
     f.nblk = 0;
-    if (x >= x1) return f;
-    const int nb = tile_blocks(s, part, tile);
-    f.part = part;
-    f.q0 = s.q0;
-    f.row0 = tile * kRows;
-    f.rows = (int)lmin(kRows, (long long)s.nq * a.G - f.row0);
-    f.kvh = kvh;
-    f.kb0 = (int)lmin(nb - 1, x - tile_x0);
-    f.nblk = (int)lmax(1, lmin(nb - f.kb0, x1 - x));
-    f.limit = tile_limit(s, part, tile);
-    f.vis_max = s.kv;
-    f.vis0 = part == 1 || !a.causal ? s.kv : s.kv - s.nq + 1;
-    f.first = f.kb0 == 0;
-    f.whole = f.first && f.nblk == nb;
-    f.n_cont = (int)((tile_x0 + nb - 1) / per - x / per);
-    f.pages = (int)(((long long)f.limit + (1 << a.b.page_shift) - 1) >> a.b.page_shift);
-    f.page_list = part == 1 ? a.b.prefix_pages : a.b.table + (long long)seq * a.b.table_stride;
-    // step
-    x += f.nblk;
-    if (x < x1 && f.kb0 + f.nblk >= nb) {
-      tile_x0 += nb;
-      if (++tile >= tiles_of(s)) {
-        tile = 0;
-        if (++kvh >= a.n_kv_heads) {
-          kvh = 0;
-          part = 0;
-          do {
-            if (++seq >= a.b.n_seqs) {
-              x = x1;   // (lengths that change while the kernel runs)
-              break;
-            }
-            s = paged_seq(a.b, seq);
-          } while (s.nq == 0);
+    while (x < x1) {
+      const int nb = tile_blocks(s, part, tile);
+      const long long b0 = tile_x0 + kTileCost;   // where block 0 lies
+      x = lmax(x, b0);
+      if (x < x1) {
+        f.part = part;
+        f.q0 = s.q0;
+        f.row0 = tile * kRows;
+        f.rows = (int)lmin(kRows, (long long)s.nq * a.G - f.row0);
+        f.tok0 = f.row0 / a.G;
+        f.rem0 = f.row0 - f.tok0 * a.G;
+        f.kvh = kvh;
+        f.kb0 = (int)lmin(nb - 1, x - b0);
+        f.nblk = (int)lmax(1, lmin(nb - f.kb0, x1 - x));
+        f.limit = tile_limit(s, part, tile);
+        f.vis_max = s.kv;
+        f.vis0 = part == 1 || !a.causal ? s.kv : s.kv - s.nq + 1;
+        f.first = f.kb0 == 0;
+        f.whole = f.first && f.nblk == nb;
+        // (the CTA of the last block is this one unless the interval ends before it)
+        f.n_cont = b0 + nb <= x1 ? 0 : (int)((b0 + nb - 1 - x1) / per) + 1;
+        f.pages = (int)(((long long)f.limit + (1 << a.b.page_shift) - 1) >> a.b.page_shift);
+        f.page_list = part == 1 ? a.b.prefix_pages : a.b.table + (long long)seq * a.b.table_stride;
+        x += f.nblk;
+      }
+      if (x < x1) {   // on to the next tile
+        tile_x0 = b0 + nb;
+        if (++tile >= tiles_of(s)) {
+          tile = 0;
+          if (++kvh >= a.n_kv_heads) {
+            kvh = 0;
+            part = 0;
+            do {
+              if (++seq >= a.b.n_seqs) {
+                x = x1;   // (lengths that change while the kernel runs)
+                break;
+              }
+              s = paged_seq(a.b, seq);
+            } while (s.nq == 0);
+          }
         }
       }
+      if (f.nblk) break;
     }
     return f;
   }
@@ -282,56 +312,103 @@ __device__ __forceinline__ PagedDest paged_dest(const PagedAttnArgs& a, const Pa
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // Joins the pieces of every row: own keys first, then the prefix, each in key
-// order.  One warp per row; reads what the pieces wrote (mostly from L2).
-template <typename T, int kHd>
+// order.  16 lanes read a piece, four pieces at a time.  kShare groups of 16
+// lanes share a row: 1 where there are rows enough for every lane, 16 (the
+// block) for a few rows, which a long context may have cut into 148 pieces.
+template <typename T, int kHd, int kShare>
 __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, int grid_main) {
+  constexpr int kPer = kHd / 16, kBatch = 4;   // columns a lane, pieces in flight
+  __shared__ float s_acc[kShare > 1 ? 16 : 1][kHd], s_ref[16], s_sum[16];
   pdl_wait();
-  constexpr int kPer = kHd / 32;   // columns a lane
-  const int lane = threadIdx.x & 31;
+  const int grp = threadIdx.x >> 4, lane = threadIdx.x & 15;
+  const int share = kShare > 1 ? grp : 0;
   const long long rows = (long long)a.b.n_tokens * a.n_heads;
   const int parts = a.b.prefix_len > 0 ? 2 : 1;
   const int lo = a.b.n_seqs > 0 ? a.b.cu_q[0] : 0, hi = a.b.n_seqs > 0 ? a.b.cu_q[a.b.n_seqs] : 0;
-  for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
+  for (long long row = ((long long)blockIdx.x * 16 + grp) / kShare; row < rows; row += (long long)gridDim.x * 16 / kShare) {
     const int tok = (int)(row / a.n_heads), head = (int)(row % a.n_heads);
     if (tok < lo || tok >= hi) continue;
-    int2 m[2];
-    m[0] = a.meta[row];
-    m[1] = parts == 2 ? a.meta[rows + row] : make_int2(-1, 0);
-    if (m[0].x < 0) continue;   // written by the main kernel
+    int cta[2], r[2], n[2] = {0, 0};   // first CTA, row in the tile, pieces
+    bool final = false;
+    for (int p = 0; p < parts; ++p) {
+      const int2 m = a.meta[p * rows + row];
+      if (p == 0) final = m.x < 0;
+      // (what a row no tile covered finds here still stays in the workspace)
+      cta[p] = min(max(m.x, 0), grid_main - 1);
+      r[p] = m.y & (kRows - 1);
+      n[p] = 1 + min(max(m.y / kRows, 0), grid_main - 1 - cta[p]);
+    }
+    if (final) continue;   // written by the main kernel
     float acc[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
     float top = -INFINITY, sum = 0.0f;   // reference and sum of 2^(lse - top)
-    auto add = [&](const float* o, float lse) {
-      if (lse == -INFINITY) return;
-      float v[kPer];
+    for (int i0 = share; i0 < n[0] + n[1]; i0 += kShare * kBatch) {
+      float4 v[kBatch][kPer / 4];
+      float lse[kBatch];
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const float2 u = *reinterpret_cast<const float2*>(o + lane * kPer + i);
-        v[i] = u.x;
-        v[i + 1] = u.y;
+      for (int u = 0; u < kBatch; ++u) {
+        int i = i0 + u * kShare;
+        lse[u] = -INFINITY;
+        if (i >= n[0] + n[1]) continue;
+        const int p = i >= n[0];
+        i -= p ? n[0] : 0;
+        const long long at = (long long)(cta[p] + i) * kRows + r[p];
+        const float* o = i == 0 ? a.part_o + (p * rows + row) * kHd : a.slot_o + at * kHd;
+        lse[u] = i == 0 ? a.part_lse[p * rows + row] : a.slot_lse[at];
+#pragma unroll
+        for (int c = 0; c < kPer / 4; ++c) v[u][c] = *reinterpret_cast<const float4*>(o + c * 64 + lane * 4);
       }
-      const float up = fmaxf(top, lse);
-      const float w0 = top == -INFINITY ? 0.0f : exp2f(top - up), w1 = exp2f(lse - up);
-      top = up;
-      sum = sum * w0 + w1;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * w0 + v[i] * w1;
-    };
-    for (int p = 0; p < parts; ++p) {
-      // (an index from a row no tile covered stays in the workspace)
-      const int c = min(max(m[p].x, 0), grid_main - 1);
-      const int r = m[p].y & (kRows - 1);
-      const int n = min(max(m[p].y / kRows, 0), grid_main - 1 - c);
-      add(a.part_o + (p * rows + row) * kHd, a.part_lse[p * rows + row]);
-      for (int i = 1; i <= n; ++i)
-        add(a.slot_o + ((long long)(c + i) * kRows + r) * kHd, a.slot_lse[(long long)(c + i) * kRows + r]);
+      for (int u = 0; u < kBatch; ++u) {
+        if (lse[u] == -INFINITY) continue;
+        const float up = fmaxf(top, lse[u]);
+        const float w0 = top == -INFINITY ? 0.0f : exp2f(top - up), w1 = exp2f(lse[u] - up);
+        top = up;
+        sum = sum * w0 + w1;
+#pragma unroll
+        for (int c = 0; c < kPer / 4; ++c) {
+          acc[c * 4] = acc[c * 4] * w0 + v[u][c].x * w1;
+          acc[c * 4 + 1] = acc[c * 4 + 1] * w0 + v[u][c].y * w1;
+          acc[c * 4 + 2] = acc[c * 4 + 2] * w0 + v[u][c].z * w1;
+          acc[c * 4 + 3] = acc[c * 4 + 3] * w0 + v[u][c].w * w1;
+        }
+      }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    T* dst = (T*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs + lane * kPer;
+    T* dst = (T*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs;
+    if (kShare == 1) {
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) dst[i] = from_f<T>(acc[i] * inv);
-    if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+      for (int c = 0; c < kPer / 4; ++c)
+        store4<T>(dst + c * 64 + lane * 4, acc[c * 4] * inv, acc[c * 4 + 1] * inv, acc[c * 4 + 2] * inv,
+                  acc[c * 4 + 3] * inv);
+      if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    } else {
+      // (the whole block is on one row: the branches above were uniform)
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < kPer / 4; ++c)
+        *reinterpret_cast<float4*>(&s_acc[grp % (kShare > 1 ? 16 : 1)][c * 64 + lane * 4]) =
+            make_float4(acc[c * 4], acc[c * 4 + 1], acc[c * 4 + 2], acc[c * 4 + 3]);
+      if (lane == 0) {
+        s_ref[grp] = top;
+        s_sum[grp] = sum;
+      }
+      __syncthreads();
+      if (threadIdx.x < kHd) {
+        float ref = -INFINITY, x = 0.0f, z = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 16; ++g) ref = fmaxf(ref, s_ref[g]);
+#pragma unroll
+        for (int g = 0; g < 16; ++g) {
+          const float w = s_ref[g] == -INFINITY ? 0.0f : exp2f(s_ref[g] - ref);
+          x += s_acc[g % (kShare > 1 ? 16 : 1)][threadIdx.x] * w;
+          z += s_sum[g] * w;
+        }
+        dst[threadIdx.x] = from_f<T>(z > 0.0f ? x / z : 0.0f);
+        if (a.lse && threadIdx.x == 0) a.lse[row] = z > 0.0f ? (ref + log2f(z)) * kLn2 : -INFINITY;
+      }
+    }
   }
 }
 
@@ -370,9 +447,9 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(PagedAttnArgs a) {
       const int r = i / (kHd / 4), c = i % (kHd / 4) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < f.rows) {
-        const int gr = f.row0 + r;
-        v = *reinterpret_cast<const float4*>((const float*)a.q + (long long)(f.q0 + gr / a.G) * a.q_ts +
-                                             (long long)(f.kvh * a.G + gr % a.G) * a.q_hs + c);
+        const int t = a.by_g.div(f.rem0 + r);
+        v = *reinterpret_cast<const float4*>((const float*)a.q + (long long)(f.q0 + f.tok0 + t) * a.q_ts +
+                                             (long long)(f.kvh * a.G + f.rem0 + r - t * a.G) * a.q_hs + c);
       }
       *reinterpret_cast<float4*>(sQ + r * kLd + c) = v;
     }
@@ -380,8 +457,7 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(PagedAttnArgs a) {
     float top[4], sum[4], o[4][4 * kOc];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int gr = f.row0 + ty * 4 + i;
-      vis[i] = min(f.vis_max, f.vis0 + gr / a.G);
+      vis[i] = min(f.vis_max, f.vis0 + f.tok0 + a.by_g.div(f.rem0 + ty * 4 + i));
       top[i] = -INFINITY;
       sum[i] = 0.0f;
 #pragma unroll
@@ -480,7 +556,7 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(PagedAttnArgs a) {
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= f.rows) continue;
-      const int gr = f.row0 + r, tok = f.q0 + gr / a.G, head = f.kvh * a.G + gr % a.G;
+      const int t = a.by_g.div(f.rem0 + r), tok = f.q0 + f.tok0 + t, head = f.kvh * a.G + f.rem0 + r - t * a.G;
       const long long row = (long long)tok * a.n_heads + head;
       const float inv = sum[i] > 0.0f ? 1.0f / sum[i] : 0.0f;
       const float l2 = sum[i] > 0.0f ? top[i] + log2f(sum[i]) : -INFINITY;

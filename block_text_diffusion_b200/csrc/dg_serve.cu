@@ -190,6 +190,15 @@ PagedSpace paged_space(int64_t n_tokens, int64_t n_heads, int64_t head_dim, bool
   return p;
 }
 
+template <typename T, int kHd>
+dg_status run_join(const PagedAttnArgs& a, int tile, cudaStream_t s) {
+  const long long rows = (long long)a.b.n_tokens * a.n_heads;
+  // a block per row while the rows do not fill the SMs
+  if (rows <= kSMs) return done(launch(k_paged_join<T, kHd, 16>, (unsigned)rows, 256, 0, s, a, tile, (int)kSMs));
+  const unsigned blocks = (unsigned)std::min<long long>((rows + 15) / 16, kSMs * 8);
+  return done(launch(k_paged_join<T, kHd, 1>, blocks, 256, 0, s, a, tile, (int)kSMs));
+}
+
 template <int kHd>
 dg_status run_paged_attention(const dg_paged_kv* c, PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e;
@@ -206,11 +215,7 @@ dg_status run_paged_attention(const dg_paged_kv* c, PagedAttnArgs& a, cudaStream
     if (e == cudaSuccess) e = launch(k_paged_attn_f32<kHd>, kSMs, 256, paged_f32_smem<kHd>(), s, a);
   }
   if (e != cudaSuccess) return done(e);
-  const long long rows = (long long)a.b.n_tokens * a.n_heads;
-  const unsigned blocks = (unsigned)std::min<long long>((rows + 7) / 8, kSMs * 8);
-  const int tile = c->dtype == DG_BF16 ? kPaRows : kPaF32Rows;
-  if (c->dtype == DG_BF16) return done(launch(k_paged_join<bf16, kHd>, blocks, 256, 0, s, a, tile, (int)kSMs));
-  return done(launch(k_paged_join<float, kHd>, blocks, 256, 0, s, a, tile, (int)kSMs));
+  return c->dtype == DG_BF16 ? run_join<bf16, kHd>(a, kPaRows, s) : run_join<float, kHd>(a, kPaF32Rows, s);
 }
 
 }  // namespace
@@ -264,7 +269,7 @@ extern "C" dg_status dg_paged_append(const dg_paged_kv* cache, const dg_paged_ba
 
 extern "C" size_t dg_paged_attention_workspace(int32_t n_tokens, int32_t n_heads, int32_t head_dim,
                                                int32_t with_prefix) {
-  if (n_tokens < 0 || n_heads < 1 || (head_dim != 64 && head_dim != 128)) return 0;
+  if (n_tokens < 0 || n_heads < 1 || n_heads > 32768 || (head_dim != 64 && head_dim != 128)) return 0;
   if ((int64_t)n_tokens * n_heads >= (int64_t)1 << 31) return 0;
   return paged_space(n_tokens, n_heads, head_dim, with_prefix != 0).total;
 }
@@ -276,7 +281,7 @@ extern "C" dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged
   if (!cache_ok(cache) || !batch_ok(cache, batch)) return DG_ERR_INVALID_ARG;
   const int hd = cache->head_dim;
   if (hd != 64 && hd != 128) return DG_ERR_UNSUPPORTED;
-  if (n_heads < 1 || n_heads % cache->n_kv_heads || !(scale > 0.0f) || scale > 1e30f) return DG_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads > 32768 || n_heads % cache->n_kv_heads || !(scale > 0.0f) || scale > 1e30f) return DG_ERR_INVALID_ARG;
   const size_t need = dg_paged_attention_workspace(batch->n_tokens, n_heads, hd, batch->prefix_len > 0);
   if (need == 0 || !workspace || workspace_bytes < need || !aligned(workspace, 256)) return DG_ERR_INVALID_ARG;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return DG_OK;
@@ -297,6 +302,7 @@ extern "C" dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged
   a.n_heads = n_heads;
   a.n_kv_heads = cache->n_kv_heads;
   a.G = n_heads / cache->n_kv_heads;
+  a.by_g.m = SmallDiv::magic((uint32_t)a.G);
   a.causal = causal != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.k_pages = cache->k;
@@ -314,13 +320,14 @@ extern "C" dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged
 extern "C" dg_status dg_test_paged_walk(const dg_paged_kv* cache, const dg_paged_batch* batch, int32_t n_heads,
                                         int32_t causal, int32_t tile_rows, int32_t* status_word, int32_t* out,
                                         int32_t cap, int32_t* n_out) {
-  if (!cache_ok(cache) || !batch_ok(cache, batch) || n_heads < 1 || n_heads % cache->n_kv_heads) return DG_ERR_INVALID_ARG;
+  if (!cache_ok(cache) || !batch_ok(cache, batch) || n_heads < 1 || n_heads > 32768 || n_heads % cache->n_kv_heads) return DG_ERR_INVALID_ARG;
   if ((tile_rows != kPaRows && tile_rows != kPaF32Rows) || !out || !n_out) return DG_ERR_INVALID_ARG;
   PagedAttnArgs a{};
   a.b = device_batch(cache, batch, status_word);
   a.n_heads = n_heads;
   a.n_kv_heads = cache->n_kv_heads;
   a.G = n_heads / cache->n_kv_heads;
+  a.by_g.m = SmallDiv::magic((uint32_t)a.G);
   a.causal = causal != 0;
   int n = 0;
   auto walk = [&](auto w) {
