@@ -5,8 +5,9 @@
 //                   TMEM lane) and epilogue;
 //   warp 8          walks the CTA's interval and loads K and V blocks of 128
 //                   keys by TMA, page by page;
-//   warp 9          issues the MMAs;
-//   warps 10, 11    query rows of A and B.
+//   warps 9, 11     issue the MMAs of A and B;
+//   warp 10         loads the query rows and clears the rows of V past the last
+//                   visible key.
 // A piece of more than 128 rows runs wide: A holds its first 128 rows, B the
 // rest, and both use every K/V block.  A piece of at most 128 rows (single
 // tokens, the end of a ragged sequence) runs split: A and B hold the same rows
@@ -115,6 +116,9 @@ __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, int* err
   tc_fence_after();
   return ok;
 }
+__device__ __forceinline__ bool pa_wait_one(uint64_t* bar, uint32_t parity, int* err) {   // one thread
+  return mbar_try_wait(bar, parity) || pa_wait_slow(bar, parity, err);
+}
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -132,7 +136,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   uint8_t* sKV = smem + 2 * C::kBytes;            // ring of K and V blocks
   uint8_t* sStage = sKV + ST * C::kBytes;         // epilogue staging
   __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], frag_full[kPaFrags], frag_empty[kPaFrags];
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], half_full, half_empty;
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], half_full, half_empty, v_last, v_tail[2], turn[2];
   __shared__ PagedFrag s_frag[kPaFrags];
   __shared__ float s_half[128][2];                // split: maximum and sum of B's half, per row
   __shared__ long long s_tmp[kPaThreads / 32 + 1];
@@ -143,15 +147,18 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   int* const err = a.b.status;
   pdl_launch();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int s = 0; s < ST; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 2); }
     for (int s = 0; s < kPaFrags; ++s) { mbar_init(&frag_full[s], 1); mbar_init(&frag_empty[s], 11); }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
-      mbar_init(&q_empty[t], 1);
+      mbar_init(&q_empty[t], 2 - t);   // A's rows serve both accumulators of a split piece
+      mbar_init(&v_tail[t], 1);
+      mbar_init(&turn[t], 1);
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_done[t], 1);
     }
+    mbar_init(&v_last, 2);
     mbar_init(&half_full, 4);
     mbar_init(&half_empty, 4);
     fence_mbar_init();
@@ -224,122 +231,166 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         __syncwarp();
       }
     }
-  } else if (warp == 9) {
-    // ---------------- MMA issue ----------------
+  } else if (warp == 9 || warp == 11) {
+    // ---------------- MMA issue: warp 9 for A, warp 11 for B ----------------
+    // One thread for each accumulator: what a thread does between two products
+    // (bookkeeping, waits, commits: a few hundred cycles) the tensor core
+    // spends on the other's.  They take turns, A first: left to themselves
+    // their MMAs interleave, both scores come late, and both softmaxes then
+    // fight for the exponential unit at the same time (385 us against 332 with
+    // one thread, 8 canvases on a 32768-token prefix).
     constexpr uint32_t kIdS = idesc_bf16(128, kPaBlk);
     constexpr uint32_t kIdO = idesc_bf16(128, kHd) | (1u << 16);   // B is MN-major
-    int cnt = 0, p_cnt0 = 0, p_cnt1 = 0, q_cnt = 0;                // q_cnt: wide pieces
-    const uint64_t q_desc = sdesc_sw128(smem_u32(sQ));
-    const uint32_t kv_addr = smem_u32(sKV);
-    for (int fi = 0; ok; ++fi) {
-      ok = pa_wait(&frag_full[fi % kPaFrags], (fi / kPaFrags) & 1, err);
-      if (!ok) break;
-      const PagedFrag& sf = s_frag[fi % kPaFrags];
-      const int n = sf.nblk, key_end = sf.limit - sf.kb0 * kPaBlk;   // visible keys, counted from the piece's start
-      const bool wide = sf.rows > 128;
-      warp_arrive(&frag_empty[fi % kPaFrags]);
-      if (n == 0) break;
-      ok = pa_wait(&q_full[0], fi & 1, err);
-      if (ok && wide) ok = pa_wait(&q_full[1], q_cnt++ & 1, err);
-      // Step h serves accumulator t = h & 1: the product with V of its block jp,
-      // then the scores of its block jq.  Wide: both accumulators walk every
-      // block; split: A the even, B the odd ones.
-      const int steps = wide ? 2 * (n + 1) : n + 2;
-      int k_slot = 0, v_slot = 0;
+    if (lane == 0) {
+      const int t = warp == 9 ? 0 : 1;
+      const uint32_t dS = tmem + t * 128, dO = tmem + 256 + t * 128;
+      const uint64_t q_base = sdesc_sw128(smem_u32(sQ)), k_base = sdesc_sw128(smem_u32(sKV)),
+                     v_base = sdesc_mn_sw128(smem_u32(sKV));
+      int slot = 0, q_cnt = 0;                      // next block of the ring; wide pieces
+      uint32_t phase = 0, p_phase = 0, tail_phase = 0, turn_phase = t ? 0 : 1;   // (A's first turn is free)
+      for (int fi = 0; ok; ++fi) {
+        ok = pa_wait_one(&frag_full[fi % kPaFrags], (fi / kPaFrags) & 1, err);
+        if (!ok) break;
+        const PagedFrag& sf = s_frag[fi % kPaFrags];
+        const int n = sf.nblk;
+        const bool wide = sf.rows > 128, tail = sf.limit < (sf.kb0 + n) * kPaBlk;
+        mbar_arrive(&frag_empty[fi % kPaFrags]);
+        if (n == 0) break;
+        // (both threads follow every phase of q_full[0], needed or not: a parity
+        // tells neighbouring phases apart, no more)
+        ok = pa_wait_one(&q_full[0], fi & 1, err);
+        if (ok && wide && t) ok = pa_wait_one(&q_full[1], q_cnt++ & 1, err);
+        const int stride = wide ? 1 : 2, j_first = wide ? 0 : t;   // split: A the even blocks, B the odd ones
+        const uint64_t qd = q_base + (wide && t ? C::kBytes >> 4 : 0);
+        if (t && (wide || n == 1)) mbar_arrive(&q_empty[0]);       // B does not read A's rows
+        // Block `at` of the piece, in ring order; those before it that only the
+        // other accumulator uses are handed on.
+        int i = 0;
+        auto step = [&]() {
+          ok = pa_wait_one(&kv_full[slot], phase, err);
+          const int s = slot;
+          if (++slot == ST) { slot = 0; phase ^= 1; }
+          ++i;
+          return s;
+        };
+        auto take = [&](int at) {
+          while (ok && i < at) mbar_arrive(&kv_empty[step()]);
+          return ok ? step() : 0;
+        };
 #pragma unroll 1
-      for (int h = 0; h < steps && ok; ++h) {
-        const int t = h & 1;
-        const int jq = wide ? h >> 1 : h, jp = wide ? jq - 1 : jq - 2;
-        const bool take = !wide || t == 0, give = !wide || t == 1;
-        if (jp >= 0) {
-          if (take) {
-            v_slot = cnt % ST;
-            ok = pa_wait(&kv_full[v_slot], (cnt / ST) & 1, err);
-            ++cnt;
-            // Keys past the last visible one are masked in S, but 0 times
-            // whatever their values hold (the cache may hold anything there)
-            // is not 0 for an infinity or a NaN: their rows of V become zeros.
-            const int valid = max(0, key_end - jp * kPaBlk);
-            if (valid < kPaBlk) {
-#pragma unroll 1
-              for (int g = 0; g < C::kHalves; ++g)
-#pragma unroll 1
-                for (int i = lane; i < (kPaBlk - valid) * 8; i += 32)
-                  *reinterpret_cast<uint4*>(sKV + v_slot * C::kBytes + g * 16384 + valid * 128 + i * 16) =
-                      make_uint4(0, 0, 0, 0);
-              fence_async_smem();
-              __syncwarp();
+        for (int j = j_first - stride; j < n && ok; j += stride) {
+          // the product with V of block j, then the scores of block jn
+          const int jn = j + stride;
+          const bool do_v = j >= 0, do_k = jn < n;
+          int v_slot = 0, k_slot = 0;
+          if (do_v) v_slot = take(wide ? 2 * j + 1 : j == n - 1 ? 2 * n - 1 : 2 * j + 2);
+          if (do_k && ok) k_slot = take(wide ? 2 * jn : jn == 0 ? 0 : 2 * jn - 1);
+          if (do_v && ok) {
+            if (tail && j == n - 1) {
+              // warp 10 clears the rows past the last key once every user of the
+              // block is here (the softmax still runs)
+              mbar_arrive(&v_last);
+              if (!wide) mbar_arrive(&v_last);
+              ok = pa_wait_one(&v_tail[t], tail_phase, err);
+              tail_phase ^= 1;
             }
+            if (ok) ok = pa_wait_one(&p_full[t], p_phase, err);
+            p_phase ^= 1;
           }
-          int& pc = t ? p_cnt1 : p_cnt0;
-          if (ok) ok = pa_wait(&p_full[t], pc++ & 1, err);
+          if (ok) ok = pa_wait_one(&turn[t], turn_phase, err);
+          turn_phase ^= 1;
           if (!ok) break;
-          if (lane == 0) {
-            const uint64_t vd = sdesc_mn_sw128(kv_addr + v_slot * C::kBytes);
-            const bool acc = wide ? jp > 0 : jp > 1;
+          tc_fence_after();
+          if (do_v) {
+            const uint64_t vd = v_base + v_slot * (C::kBytes >> 4);
+            const uint32_t acc = j > j_first ? 1u : 0u;
 #pragma unroll
             for (int kk = 0; kk < kPaBlk / 16; ++kk)
-              tc_mma_bf16_ta(tmem + 256 + t * 128, tmem + t * 128 + kk * 8, vd + kk * (2048 >> 4), kIdO,
-                             acc || kk > 0 ? 1u : 0u);
-            if (give) tc_commit(&kv_empty[v_slot]);
-            if (jq >= n) tc_commit(&o_done[t]);
+              tc_mma_bf16_ta(dO, dS + kk * 8, vd + kk * (2048 >> 4), kIdO, kk > 0 ? 1u : acc);
           }
-        }
-        if (jq < n) {
-          if (take) {
-            k_slot = cnt % ST;
-            ok = pa_wait(&kv_full[k_slot], (cnt / ST) & 1, err);
-            ++cnt;
-          }
-          if (!ok) break;
-          if (lane == 0) {
-            const uint64_t qd = q_desc + (wide && t ? C::kBytes >> 4 : 0);
-            const uint64_t kd = sdesc_sw128(kv_addr + k_slot * C::kBytes);
+          if (do_k) {
+            const uint64_t kd = k_base + k_slot * (C::kBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < kHd / 16; ++kk)
-              tc_mma_bf16(tmem + t * 128, qd + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3),
-                          kd + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3), kIdS, kk > 0 ? 1u : 0u);
-            tc_commit(&s_full[t]);
-            if (give) tc_commit(&kv_empty[k_slot]);
-            // the query rows' space is free after the last scores
-            if (jq == n - 1) tc_commit(&q_empty[wide ? t : 0]);
+              tc_mma_bf16(dS, qd + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3), kd + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3),
+                          kIdS, kk > 0 ? 1u : 0u);
           }
+          mbar_arrive(&turn[1 - t]);
+          if (do_k) {
+            tc_commit(&s_full[t]);
+            tc_commit(&kv_empty[k_slot]);
+            if (jn + stride >= n) tc_commit(&q_empty[wide ? t : 0]);   // the query rows' space is free
+          } else if (do_v) {
+            tc_commit(&o_done[t]);
+          }
+          if (do_v) tc_commit(&kv_empty[v_slot]);
         }
-        __syncwarp();
+        while (ok && i < 2 * n) mbar_arrive(&kv_empty[step()]);
+        if (ok && t && !wide && (n & 1)) {          // A had one turn more
+          ok = pa_wait_one(&turn[1], turn_phase, err);
+          turn_phase ^= 1;
+          mbar_arrive(&turn[0]);
+        }
       }
     }
-  } else if (warp >= 10) {
+    __syncwarp();
+  } else if (warp == 10) {
     // ---------------- query rows ----------------
     // 16 bytes at a time, asynchronously, in the layout the MMA reads.  Rows
     // past the piece's end keep what is there: no row of the products mixes
     // with another.
-    const int t = warp - 10;
     constexpr int kPer = kHd / 8, kAt = 32 / kPer;   // chunks a row, rows a pass of the warp
     const int c = lane % kPer;
-    const uint32_t dst = smem_u32(sQ + t * C::kBytes) + (c >> 3) * 16384;
-    int used = 0;   // pieces this warp has loaded for
+    const uint32_t dst = smem_u32(sQ) + (c >> 3) * 16384;
+    int used[2] = {0, 0}, blocks = 0, tails = 0;     // pieces loaded for; K and V blocks up to this piece; tails cleared
     for (int fi = 0; ok; ++fi) {
       ok = pa_wait(&frag_full[fi % kPaFrags], (fi / kPaFrags) & 1, err);
       if (!ok) break;
       const PagedFrag& sf = s_frag[fi % kPaFrags];
-      const int n = sf.nblk, first = t * 128, rows = min(128, sf.rows - first), rem0 = sf.rem0;
+      const int n = sf.nblk, rows = sf.rows, rem0 = sf.rem0;
+      const int valid = max(0, sf.limit - (sf.kb0 + n - 1) * kPaBlk);   // visible keys of the last block
       const bf16* src = (const bf16*)a.q + (long long)(sf.q0 + sf.tok0) * a.q_ts +
                         (long long)(sf.kvh * a.G + rem0) * a.q_hs + c * 8;
       warp_arrive(&frag_empty[fi % kPaFrags]);
       if (n == 0) break;
-      if (rows <= 0) continue;   // B of a split piece
-      if (used > 0) ok = pa_wait(&q_empty[t], (used - 1) & 1, err);
-      if (!ok) break;
-      ++used;
+      blocks += 2 * n;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t * 128 >= rows || !ok) continue;   // no B in a split piece
+        if (used[t] > 0) ok = pa_wait(&q_empty[t], (used[t] - 1) & 1, err);
+        if (!ok) continue;
+        ++used[t];
+        const int last = min(rows, t * 128 + 128);
 #pragma unroll 4
-      for (int row = lane / kPer; row < rows; row += kAt) {
-        const int tk = a.by_g.div(rem0 + first + row);
-        cp_async_16(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-                    src + (long long)tk * a.q_ts + (long long)(first + row - tk * a.G) * a.q_hs);
+        for (int row = t * 128 + lane / kPer; row < last; row += kAt) {
+          const int tk = a.by_g.div(rem0 + row);
+          cp_async_16(dst + row * 128 + t * (C::kBytes - 16384) + (((c & 7) ^ (row & 7)) << 4),
+                      src + (long long)tk * a.q_ts + (long long)(row - tk * a.G) * a.q_hs);
+        }
+        cp_async_wait_all();
+        fence_async_smem();
+        warp_arrive(&q_full[t]);
       }
-      cp_async_wait_all();
-      fence_async_smem();
-      warp_arrive(&q_full[t]);
+      if (ok && valid < kPaBlk) {
+        // Keys past the last visible one are masked in S, but 0 times whatever
+        // their values hold (the cache may hold anything there) is not 0 for an
+        // infinity or a NaN: their rows of V, the piece's last block, become zeros.
+        const int s = (blocks - 1) % ST;
+        ok = pa_wait(&v_last, tails++ & 1, err);
+        if (!ok) break;
+#pragma unroll 1
+        for (int i = lane; i < (kPaBlk - valid) * 8 * C::kHalves; i += 32) {
+          const int g = i / ((kPaBlk - valid) * 8), at = i - g * ((kPaBlk - valid) * 8);
+          *reinterpret_cast<uint4*>(sKV + s * C::kBytes + g * 16384 + valid * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+        const bool wide = rows > 128;
+        if (lane == 0) {
+          if (wide || ((n - 1) & 1) == 0) mbar_arrive(&v_tail[0]);
+          if (wide || ((n - 1) & 1) == 1) mbar_arrive(&v_tail[1]);
+        }
+      }
     }
   } else {
     // ---------------- softmax ----------------
