@@ -30,6 +30,7 @@
 constexpr int kPaThreads = 384;
 constexpr int kPaRows = 256, kPaBlk = 128;
 constexpr int kPaFrags = 4;       // pieces announced ahead
+constexpr int kPaPart = 96;       // keys of a block whose probabilities go to the MMA before the rest
 constexpr int kPaStage = 4096;    // epilogue staging of a softmax warp: 32 rows x 128 bytes
 
 template <int kHd>
@@ -96,6 +97,12 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t* r) 
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -136,7 +143,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   uint8_t* sKV = smem + 2 * C::kBytes;            // ring of K and V blocks
   uint8_t* sStage = sKV + ST * C::kBytes;         // epilogue staging
   __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], frag_full[kPaFrags], frag_empty[kPaFrags];
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_done[2], half_full, half_empty, v_last, v_tail[2], turn[2];
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], o_done[2], half_full, half_empty, v_last, v_tail[2], turn[2][4];
   __shared__ PagedFrag s_frag[kPaFrags];
   __shared__ float s_half[128][2];                // split: maximum and sum of B's half, per row
   __shared__ long long s_tmp[kPaThreads / 32 + 1];
@@ -153,8 +160,9 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 2 - t);   // A's rows serve both accumulators of a split piece
       mbar_init(&v_tail[t], 1);
-      mbar_init(&turn[t], 1);
+      for (int w = 0; w < 4; ++w) mbar_init(&turn[t][w], 1);
       mbar_init(&s_full[t], 1);
+      mbar_init(&p_part[t], 4);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_done[t], 1);
     }
@@ -235,10 +243,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     // ---------------- MMA issue: warp 9 for A, warp 11 for B ----------------
     // One thread for each accumulator: what a thread does between two products
     // (bookkeeping, waits, commits: a few hundred cycles) the tensor core
-    // spends on the other's.  They take turns, A first: left to themselves
-    // their MMAs interleave, both scores come late, and both softmaxes then
-    // fight for the exponential unit at the same time (385 us against 332 with
-    // one thread, 8 canvases on a 32768-token prefix).
+    // spends on the other's.
     constexpr uint32_t kIdS = idesc_bf16(128, kPaBlk);
     constexpr uint32_t kIdO = idesc_bf16(128, kHd) | (1u << 16);   // B is MN-major
     if (lane == 0) {
@@ -247,7 +252,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const uint64_t q_base = sdesc_sw128(smem_u32(sQ)), k_base = sdesc_sw128(smem_u32(sKV)),
                      v_base = sdesc_mn_sw128(smem_u32(sKV));
       int slot = 0, q_cnt = 0;                      // next block of the ring; wide pieces
-      uint32_t phase = 0, p_phase = 0, tail_phase = 0, turn_phase = t ? 0 : 1;   // (A's first turn is free)
+      uint32_t phase = 0, p_phase = 0, tail_phase = 0;
       for (int fi = 0; ok; ++fi) {
         ok = pa_wait_one(&frag_full[fi % kPaFrags], (fi / kPaFrags) & 1, err);
         if (!ok) break;
@@ -294,19 +299,27 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               ok = pa_wait_one(&v_tail[t], tail_phase, err);
               tail_phase ^= 1;
             }
-            if (ok) ok = pa_wait_one(&p_full[t], p_phase, err);
-            p_phase ^= 1;
           }
-          if (ok) ok = pa_wait_one(&turn[t], turn_phase, err);
-          turn_phase ^= 1;
           if (!ok) break;
           tc_fence_after();
           if (do_v) {
+            // P comes in two parts (see kPaPart), so most of the product runs
+            // under the exponentials of the rest
             const uint64_t vd = v_base + v_slot * (C::kBytes >> 4);
             const uint32_t acc = j > j_first ? 1u : 0u;
+            ok = pa_wait_one(&p_part[t], p_phase, err);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < kPaBlk / 16; ++kk)
+            for (int kk = 0; kk < kPaPart / 16; ++kk)
               tc_mma_bf16_ta(dO, dS + kk * 8, vd + kk * (2048 >> 4), kIdO, kk > 0 ? 1u : acc);
+            ok = pa_wait_one(&p_full[t], p_phase, err);
+            p_phase ^= 1;
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = kPaPart / 16; kk < kPaBlk / 16; ++kk)
+              tc_mma_bf16_ta(dO, dS + kk * 8, vd + kk * (2048 >> 4), kIdO, 1u);
           }
           if (do_k) {
             const uint64_t kd = k_base + k_slot * (C::kBytes >> 4);
@@ -314,9 +327,6 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             for (int kk = 0; kk < kHd / 16; ++kk)
               tc_mma_bf16(dS, qd + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3), kd + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3),
                           kIdS, kk > 0 ? 1u : 0u);
-          }
-          mbar_arrive(&turn[1 - t]);
-          if (do_k) {
             tc_commit(&s_full[t]);
             tc_commit(&kv_empty[k_slot]);
             if (jn + stride >= n) tc_commit(&q_empty[wide ? t : 0]);   // the query rows' space is free
@@ -326,11 +336,6 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           if (do_v) tc_commit(&kv_empty[v_slot]);
         }
         while (ok && i < 2 * n) mbar_arrive(&kv_empty[step()]);
-        if (ok && t && !wide && (n & 1)) {          // A had one turn more
-          ok = pa_wait_one(&turn[1], turn_phase, err);
-          turn_phase ^= 1;
-          mbar_arrive(&turn[0]);
-        }
       }
     }
     __syncwarp();
@@ -399,6 +404,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const uint32_t lane_off = (uint32_t)(wt * 32) << 16;
     const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * 128 + lane_off;
     int s_cnt = 0, done_cnt = 0, half_cnt = 0;
+    uint32_t turn_phase = t ? 0 : 1;               // (A's first turn is free)
     for (int fi = 0; ok; ++fi) {
       ok = pa_wait(&frag_full[fi % kPaFrags], (fi / kPaFrags) & 1, err);
       if (!ok) break;
@@ -433,13 +439,13 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
           float mt[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mt[c] = __uint_as_float(w[c]);
+          for (int u = 0; u < 4; ++u) mt[u] = __uint_as_float(w[u]);
 #pragma unroll
-          for (int c = 4; c < kPaBlk; c += 8)
+          for (int c = 4; c < kPaBlk - 4; c += 8)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              mt[u] = fmaxf(mt[u], c + u + 4 < kPaBlk ? fmaxf(__uint_as_float(w[c + u]), __uint_as_float(w[c + u + 4]))
-                                                      : __uint_as_float(w[c + u]));
+            for (int u = 0; u < 4; ++u) mt[u] = max3(mt[u], __uint_as_float(w[c + u]), __uint_as_float(w[c + u + 4]));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mt[u] = fmaxf(mt[u], __uint_as_float(w[kPaBlk - 4 + u]));
           const float mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * a.scale_log2;
           // The reference moves only when the block's maximum passes it by more
           // than 8 (P stays below 256), so O is rarely rescaled; the sum uses
@@ -447,40 +453,62 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           const float m_new = (m_run == -INFINITY || mx > m_run + 8.0f) ? mx : m_run;
           const float alpha = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m_new);
           const float nm = m_new == -INFINITY ? 0.0f : -m_new;
+          // S(j) was complete, so the PV before it, issued earlier, was too: O is ours
+          if (j > j0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+            for (int q = 0; q < kHd; q += 16) {
+              uint32_t o[16];
+              tmem_ld16_nw(tO + q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
+              tmem_st16_nw(tO + q, o);
+            }
+          }
+          // The exponential unit is what both softmaxes need most; the warps of A
+          // and B on it take turns, so one exponentiates while the other's MMAs run.
+          ok = pa_wait(&turn[t][wt], turn_phase, err);
+          turn_phase ^= 1;
+          if (!ok) break;
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
           // P is rounded to bf16 for the MMA (its operands are 16-bit); the row
           // sum adds the fp32 values
 #pragma unroll
-          for (int ch = 0; ch < kPaBlk; ch += 64) {
-            uint32_t pk[32];
+          for (int ch = 0; ch < kPaBlk; ch += 32) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
+            for (int q = 0; q < 16; ++q) {
               const float p0 = ex2_approx(fmaf(__uint_as_float(w[ch + 2 * q]), a.scale_log2, nm));
               const float p1 = ex2_approx(fmaf(__uint_as_float(w[ch + 2 * q + 1]), a.scale_log2, nm));
               ls[q & 3] += p0 + p1;
               const __nv_bfloat162 pr = __floats2bfloat162_rn(p0, p1);
               pk[q] = *reinterpret_cast<const uint32_t*>(&pr);
             }
-            tmem_st32_nw(tS + ch / 2, pk);
-          }
-          // S(j) was complete, so the PV before it, issued earlier, was too: O is ours
-          if (j > j0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll 1
-            for (int q = 0; q < kHd; q += 32) {
-              uint32_t o[32];
-              tmem_ld32_nw(tO + q, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * alpha);
-              tmem_st32_nw(tO + q, o);
+            tmem_st16_nw(tS + ch / 2, pk);
+            if (ch + 32 == kPaPart) {
+              tmem_wait_st();
+              tc_fence_before();
+              warp_arrive(&p_part[t]);
             }
           }
+          if (lane == 0) mbar_arrive(&turn[1 - t][wt]);
           l_run = l_run * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
           m_run = m_new;
           tmem_wait_st();
+        } else {
+          ok = pa_wait(&turn[t][wt], turn_phase, err);
+          turn_phase ^= 1;
+          if (!ok) break;
+          warp_arrive(&turn[1 - t][wt]);
+          warp_arrive(&p_part[t]);
         }
         tc_fence_before();
         warp_arrive(&p_full[t]);
+      }
+      if (ok && split && t == 1 && (nblk & 1)) {     // A had one turn more
+        ok = pa_wait(&turn[1][wt], turn_phase, err);
+        turn_phase ^= 1;
+        if (ok) warp_arrive(&turn[0][wt]);
       }
       // ---------------- epilogue ----------------
       const bool both = split && nblk > 1;           // B has a half to join
