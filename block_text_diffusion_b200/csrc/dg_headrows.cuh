@@ -22,6 +22,7 @@ struct HeadRows {
 
 struct HeadRowsArgs {
   int n_tokens, n_q, n_k, n_v, head_dim;   // heads of each kind (n_v: copied values, append only)
+  float inv_dim;                           // 1 / head_dim
   HeadRows q, qo, k, ko, v;
   const int* positions;
   // rotation
@@ -210,31 +211,60 @@ template <> struct Chunk<bf16> {
   }
 };
 
+// Two binary32 operations in one instruction (sm_100).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // Whole 16-byte chunks: a lane holds two chunks of a head, and in the half
 // layout the second one holds the partners of the first, so a rotation needs
 // no exchange between lanes.  head_dim / (2 * chunk) lanes (a power of two)
-// share a head; a warp takes `kGroups` groups of 32 / lanes heads of one token,
-// computes the token's sines and cosines once and has every load of its heads
-// in flight before it needs the first.
-template <typename T, int kGroups>
-__global__ void __launch_bounds__(256) k_head_rows(HeadRowsArgs a, int lph_shift, int warps_per_token) {
+// share a head, a warp takes 32 / lanes heads (a group) at once and kGroups
+// groups of one kind (a batch) with all their loads in flight.
+//
+// With u, v a pair, gains gu, gv and r = 1 / rms:
+//   u' = r (u gu c - v gv s),   v' = r (v gv c + u gu s);
+// the four products of gain and sine or cosine belong to the lane and the
+// token, not to the head, so they are formed once a batch, and two pairs go
+// through one packed instruction.
+//
+// Bound by memory when there are many tokens (26B heads, 8192 tokens: one
+// read and one write of 50 MB each), by the launch and two dependent reads
+// when there are few.  Forming the gains and phases for every head took 1340
+// instructions a warp and 41 us; this form takes fewer than half.
+template <typename T, int kGroups, bool kInter>
+__global__ void __launch_bounds__(256, 2) k_head_rows(const __grid_constant__ HeadRowsArgs a, int lph_shift,
+                                                       unsigned warps_per_token, int batches_per_warp) {
   constexpr int N = Chunk<T>::kN;
   __shared__ __align__(16) float s_cos[8][128], s_sin[8][128];
   pdl_enter();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + warp;
-  const int t = (int)(w / warps_per_token);
+  const unsigned w = blockIdx.x * 8u + warp;
+  const int t = (int)(warps_per_token == 1 ? w : w / warps_per_token);
   if (t >= a.n_tokens) return;
   const int lph = 1 << lph_shift, hpw = 32 >> lph_shift;   // lanes a head, heads a group
   const int j = lane & (lph - 1), sub = lane >> lph_shift;
-  const int gq = (a.n_q + hpw - 1) / hpw, gk = (a.n_k + hpw - 1) / hpw, gv = (a.n_v + hpw - 1) / hpw;
-  const int g0 = (int)(w % warps_per_token) * kGroups;
+  const int batch_shift = 5 - lph_shift + (kGroups == 4 ? 2 : 0), per_batch = 1 << batch_shift;   // heads
+  const int bq = (a.n_q + per_batch - 1) >> batch_shift, bk = (a.n_k + per_batch - 1) >> batch_shift,
+            bv = (a.n_v + per_batch - 1) >> batch_shift;
+  const int b0 = (int)(warps_per_token == 1 ? 0 : w - t * warps_per_token) * batches_per_warp,
+            b1 = min(b0 + batches_per_warp, bq + bk + bv);
 
-  // chunks of the lane; rotated chunks and their partners first
+  // chunks of the lane; in the half layout rotated chunks and their partners first
   const int rp = a.rot_dim / 2, rc = rp / N;          // rotated pairs, chunks of them (half layout)
   int ca = j, cb = j + lph;
   bool turn_a, turn_b;
-  if (a.interleaved) {
+  if (kInter) {
     turn_a = ca * N < a.rot_dim;
     turn_b = cb * N < a.rot_dim;
   } else {
@@ -246,110 +276,149 @@ __global__ void __launch_bounds__(256) k_head_rows(HeadRowsArgs a, int lph_shift
     }
   }
 
-  uint4 xa[kGroups] = {}, xb[kGroups] = {};
-  int kind[kGroups], head[kGroups];
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const int g = g0 + i;
-    kind[i] = g < gq ? 0 : g < gq + gk ? 1 : g < gq + gk + gv ? 2 : 3;
-    head[i] = (g - (kind[i] == 0 ? 0 : kind[i] == 1 ? gq : gq + gk)) * hpw + sub;
-    if (kind[i] == 3 || head[i] >= (kind[i] == 0 ? a.n_q : a.n_k)) head[i] = -1;
-    if (head[i] >= 0) {
-      const HeadRows in = kind[i] == 0 ? a.q : kind[i] == 1 ? a.k : a.v;
-      const uint4* src = reinterpret_cast<const uint4*>((const T*)in.data + (long long)t * in.ts +
-                                                        (long long)head[i] * in.hs);
-      xa[i] = src[ca];
-      xb[i] = src[cb];
-    }
-  }
-  const TokenSpot spot = token_spot(a, t);
-  if (!spot.live) return;
+  const bool all_turn = __all_sync(0xffffffffu, turn_a && turn_b);
+
+  TokenSpot spot;
+  bool have_spot = false;
   float c[N], s[N];
-  if (rp > 0 && g0 < gq + gk) {
-    for (int p = lane; p < rp; p += 32)
-      turn_sincos(spot.pos, a.inv_freq[p], a.amplitude, s_cos[warp][p], s_sin[warp][p]);
-    __syncwarp();
-    const int pa = a.interleaved ? ca * (N / 2) : j * N, pb = a.interleaved ? cb * (N / 2) : j * N + N / 2;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int kind = b < bq ? 0 : b < bq + bk ? 1 : 2;
+    const int n = kind == 0 ? a.n_q : a.n_k;
+    const int h0 = (b - (kind == 0 ? 0 : kind == 1 ? bq : bq + bk)) * per_batch + sub;
+    const HeadRows in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+    // (heads past n read the last one: no branches)
+    const T* src = (const T*)in.data + (long long)t * in.ts;
+    uint4 xa[kGroups], xb[kGroups];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool on = i < N / 2 ? turn_a : turn_b;
-      const int p = i < N / 2 ? pa + i : pb + i - N / 2;
-      c[i] = on ? s_cos[warp][p] : 1.0f;
-      s[i] = on ? s_sin[warp][p] : 0.0f;
+    for (int i = 0; i < kGroups; ++i) {
+      const uint4* at = reinterpret_cast<const uint4*>(src + (long long)min(h0 + i * hpw, n - 1) * in.hs);
+      xa[i] = at[ca];
+      xb[i] = at[cb];
     }
-  }
+    if (!have_spot) {
+      have_spot = true;
+      spot = token_spot(a, t);
+      if (!spot.live) return;
+      if (rp > 0 && kind < 2) {
+        for (int p = lane; p < rp; p += 32)
+          turn_sincos(spot.pos, a.inv_freq[p], a.amplitude, s_cos[warp][p], s_sin[warp][p]);
+        __syncwarp();
+        const int pa = kInter ? ca * (N / 2) : j * N, pb = kInter ? cb * (N / 2) : j * N + N / 2;
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    if (kind[i] == 3) break;
-    T* dst = nullptr;
-    if (head[i] >= 0) {
-      if (kind[i] == 0 || !a.paged) {
-        const HeadRows out = kind[i] == 0 ? a.qo : a.ko;
-        dst = (T*)out.data + (long long)t * out.ts + (long long)head[i] * out.hs;
-      } else if (spot.page >= 0) {
-        dst = (T*)(kind[i] == 1 ? a.k_pages : a.v_pages) +
-              (((spot.page * a.n_k + head[i]) << a.b.page_shift) + spot.off) * a.head_dim;
+        for (int e = 0; e < N / 2; e += 2) {
+          const float2 c0 = *reinterpret_cast<const float2*>(&s_cos[warp][pa + e]),
+                       c1 = *reinterpret_cast<const float2*>(&s_cos[warp][pb + e]),
+                       s0 = *reinterpret_cast<const float2*>(&s_sin[warp][pa + e]),
+                       s1 = *reinterpret_cast<const float2*>(&s_sin[warp][pb + e]);
+          c[e] = c0.x; c[e + 1] = c0.y; c[N / 2 + e] = c1.x; c[N / 2 + e + 1] = c1.y;
+          s[e] = s0.x; s[e + 1] = s0.y; s[N / 2 + e] = s1.x; s[N / 2 + e + 1] = s1.y;
+        }
+      }
+      // parts that do not turn keep their gain alone
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (!(e < N / 2 ? turn_a : turn_b)) { c[e] = 1.0f; s[e] = 0.0f; }
+    }
+    T* dst;
+    long long out_hs;
+    if (kind == 0 || !a.paged) {
+      const HeadRows out = kind == 0 ? a.qo : a.ko;
+      dst = (T*)out.data + (long long)t * out.ts;
+      out_hs = out.hs;
+    } else {
+      if (spot.page < 0) continue;
+      dst = (T*)(kind == 1 ? a.k_pages : a.v_pages) + (((spot.page * a.n_k) << a.b.page_shift) + spot.off) * a.head_dim;
+      out_hs = (long long)a.head_dim << a.b.page_shift;
+    }
+    dst += h0 * out_hs;
+    const long long out_step = out_hs << (5 - lph_shift);
+    if (kind == 2) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i, dst += out_step)
+        if (h0 + i * hpw < n) {
+          reinterpret_cast<uint4*>(dst)[ca] = xa[i];
+          reinterpret_cast<uint4*>(dst)[cb] = xb[i];
+        }
+      continue;
+    }
+    // the lane's pair e is (u, v): half layout elements e of both chunks,
+    // interleaved neighbours of chunk a (e < N / 2) or b
+    float2 uc[N / 2], vs[N / 2], vc[N / 2], us[N / 2];
+    {
+      float ga[N], gb[N];
+      const uint4* gain = reinterpret_cast<const uint4*>(kind == 0 ? a.q_gain : a.k_gain);
+      if (a.norm && gain) {
+        Chunk<T>::unpack(gain[ca], ga);
+        Chunk<T>::unpack(gain[cb], gb);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) ga[e] = gb[e] = 1.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        const float2 u = kInter ? (e < N / 2 ? make_float2(ga[2 * e], ga[2 * e + 2])
+                                             : make_float2(gb[2 * e - N], gb[2 * e - N + 2]))
+                                : make_float2(ga[e], ga[e + 1]);
+        const float2 v = kInter ? (e < N / 2 ? make_float2(ga[2 * e + 1], ga[2 * e + 3])
+                                             : make_float2(gb[2 * e - N + 1], gb[2 * e - N + 3]))
+                                : make_float2(gb[e], gb[e + 1]);
+        uc[e / 2] = mul2(u, make_float2(c[e], c[e + 1]));
+        us[e / 2] = mul2(u, make_float2(s[e], s[e + 1]));
+        vc[e / 2] = mul2(v, make_float2(c[e], c[e + 1]));
+        vs[e / 2] = mul2(v, make_float2(-s[e], -s[e + 1]));
       }
     }
-    uint4 oa = xa[i], ob = xb[i];
-    if (kind[i] < 2) {
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i, dst += out_step) {
+      if (h0 - sub + i * hpw >= n) break;
       float x[N], y[N];
       Chunk<T>::unpack(xa[i], x);
       Chunk<T>::unpack(xb[i], y);
+      float r = 1.0f;
       if (a.norm) {
-        float ss = 0.0f;
+        float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int e = 0; e < N; ++e) ss += x[e] * x[e] + y[e] * y[e];
-        for (int o = lph >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = rsqrtf(ss / (float)a.head_dim + a.eps);
-        const uint4* gain = reinterpret_cast<const uint4*>(kind[i] == 0 ? a.q_gain : a.k_gain);
-        if (gain) {
-          float ga[N], gb[N];
-          Chunk<T>::unpack(gain[ca], ga);
-          Chunk<T>::unpack(gain[cb], gb);
+        for (int e = 0; e < N; e += 2) {
+          ss = fma2(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), ss);
+          ss = fma2(make_float2(y[e], y[e + 1]), make_float2(y[e], y[e + 1]), ss);
+        }
+        float z = ss.x + ss.y;
+        for (int o = lph >> 1; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        r = rsqrtf(fmaf(z, a.inv_dim, a.eps));
+      }
+      const float2 rr = make_float2(r, r);
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            x[e] *= r * ga[e];
-            y[e] *= r * gb[e];
-          }
+      for (int e = 0; e < N; e += 2) {
+        float2 u, v;
+        if (kInter) {
+          const int k = e < N / 2 ? 2 * e : 2 * e - N;
+          u = e < N / 2 ? make_float2(x[k], x[k + 2]) : make_float2(y[k], y[k + 2]);
+          v = e < N / 2 ? make_float2(x[k + 1], x[k + 3]) : make_float2(y[k + 1], y[k + 3]);
         } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            x[e] *= r;
-            y[e] *= r;
-          }
+          u = make_float2(x[e], x[e + 1]);
+          v = make_float2(y[e], y[e + 1]);
+        }
+        float2 un = mul2(u, uc[e / 2]), vn = mul2(v, vc[e / 2]);
+        // (a part that does not turn takes nothing from its partner, not even 0 times an infinity)
+        if (all_turn || (e < N / 2 ? turn_a : turn_b)) {
+          un = fma2(v, vs[e / 2], un);
+          vn = fma2(u, us[e / 2], vn);
+        }
+        un = mul2(un, rr);
+        vn = mul2(vn, rr);
+        if (kInter) {
+          const int k = e < N / 2 ? 2 * e : 2 * e - N;
+          float(&z)[N] = e < N / 2 ? x : y;
+          z[k] = un.x; z[k + 2] = un.y; z[k + 1] = vn.x; z[k + 3] = vn.y;
+        } else {
+          x[e] = un.x; x[e + 1] = un.y; y[e] = vn.x; y[e + 1] = vn.y;
         }
       }
-      if (rp > 0) {
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < N / 2; ++e) {
-            if (turn_a) {
-              const float u = x[2 * e], v = x[2 * e + 1];
-              x[2 * e] = u * c[e] - v * s[e];
-              x[2 * e + 1] = v * c[e] + u * s[e];
-            }
-            if (turn_b) {
-              const float u = y[2 * e], v = y[2 * e + 1];
-              y[2 * e] = u * c[N / 2 + e] - v * s[N / 2 + e];
-              y[2 * e + 1] = v * c[N / 2 + e] + u * s[N / 2 + e];
-            }
-          }
-        } else if (turn_a) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float u = x[e], v = y[e];
-            x[e] = u * c[e] - v * s[e];
-            y[e] = v * c[e] + u * s[e];
-          }
-        }
+      if (h0 + i * hpw < n) {
+        reinterpret_cast<uint4*>(dst)[ca] = Chunk<T>::pack(x);
+        reinterpret_cast<uint4*>(dst)[cb] = Chunk<T>::pack(y);
       }
-      oa = Chunk<T>::pack(x);
-      ob = Chunk<T>::pack(y);
-    }
-    if (dst) {
-      reinterpret_cast<uint4*>(dst)[ca] = oa;
-      reinterpret_cast<uint4*>(dst)[cb] = ob;
     }
   }
 }

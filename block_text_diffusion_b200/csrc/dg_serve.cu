@@ -152,19 +152,29 @@ dg_status run_head_rows(const HeadRowsArgs& a, cudaStream_t s) {
   }
   int shift = 0;
   while ((1 << shift) < lph) ++shift;
+  // Batches of `groups` x 32 / lph heads of one kind; a warp takes one batch
+  // while the batches do not fill the SMs, all of its token's when they do
+  // (its sines and cosines then serve every head).
   const int hpw = 32 / lph;
-  auto groups = [&](int n) { return (n + hpw - 1) / hpw; };
-  const int g = groups(a.n_q) + groups(a.n_k) + groups(a.n_v);
-  const bool many = (long long)a.n_tokens * g > kSMs * 32;
-  const int per = many ? 4 : 1;
-  const int wpt = (g + per - 1) / per;
+  auto batches = [&](int groups) {
+    auto of = [&](int n) { return (n + hpw * groups - 1) / (hpw * groups); };
+    return of(a.n_q) + of(a.n_k) + of(a.n_v);
+  };
+  const bool many = (long long)a.n_tokens * batches(1) > kSMs * 32;
+  const int nb = batches(many ? 4 : 1), per = many ? nb : 1;
+  const int wpt = (nb + per - 1) / per;
   const long long blocks = ((long long)a.n_tokens * wpt + 7) / 8;
-  if (blocks >= (1ll << 31)) return DG_ERR_INVALID_ARG;
-  return done(many ? launch(k_head_rows<T, 4>, (unsigned)blocks, 256, 0, s, a, shift, wpt)
-                   : launch(k_head_rows<T, 1>, (unsigned)blocks, 256, 0, s, a, shift, wpt));
+  if (blocks >= (1ll << 28)) return DG_ERR_INVALID_ARG;   // (warps are counted in 32 bits)
+  const unsigned g = (unsigned)blocks;
+  if (a.interleaved)
+    return done(many ? launch(k_head_rows<T, 4, true>, g, 256, 0, s, a, shift, (unsigned)wpt, per)
+                     : launch(k_head_rows<T, 1, true>, g, 256, 0, s, a, shift, (unsigned)wpt, per));
+  return done(many ? launch(k_head_rows<T, 4, false>, g, 256, 0, s, a, shift, (unsigned)wpt, per)
+                   : launch(k_head_rows<T, 1, false>, g, 256, 0, s, a, shift, (unsigned)wpt, per));
 }
 
-dg_status run_head_rows(int dtype, const HeadRowsArgs& a, cudaStream_t s) {
+dg_status run_head_rows(int dtype, HeadRowsArgs& a, cudaStream_t s) {
+  a.inv_dim = 1.0f / (float)a.head_dim;
   return dtype == DG_BF16 ? run_head_rows<bf16>(a, s) : run_head_rows<float>(a, s);
 }
 
