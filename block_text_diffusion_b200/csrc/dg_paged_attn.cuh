@@ -92,16 +92,17 @@ struct PagedWalk {
 
   DG_HD PagedWalk(const PagedAttnArgs& a_) : a(a_) {}
 
-  DG_HD int tiles_of(const PagedSeq& q) const { return (int)(((long long)q.nq * a.G + kRows - 1) / kRows); }
+  // (rows of a sequence are at most n_tokens * n_heads < 2^31: 32-bit arithmetic)
+  DG_HD int tiles_of(const PagedSeq& q) const { return (int)(((unsigned)(q.nq * a.G) + kRows - 1) / kRows); }
   // keys visible to the last row of a tile of the current sequence
   DG_HD int tile_limit(const PagedSeq& q, int part_, int tl) const {
     if (part_ == 1 || !a.causal) return q.kv;
-    const long long last = lmin((long long)(tl + 1) * kRows, (long long)q.nq * a.G) - 1;
-    return imax(0, q.kv - q.nq + (int)(last / a.G) + 1);
+    const unsigned rows = (unsigned)(q.nq * a.G), end = (unsigned)(tl + 1) * kRows;
+    return imax(0, q.kv - q.nq + (int)(((end < rows ? end : rows) - 1) / (unsigned)a.G) + 1);
   }
   // A tile whose rows see nothing keeps one (masked) block: it writes its zeros.
   DG_HD int tile_blocks(const PagedSeq& q, int part_, int tl) const {
-    return imax(1, (int)(((long long)tile_limit(q, part_, tl) + kBlk - 1) / kBlk));
+    return imax(1, (int)(((unsigned)tile_limit(q, part_, tl) + kBlk - 1) / kBlk));
   }
   // units of all tiles of one sequence for one key head
   DG_HD long long seq_units(const PagedSeq& q, int part_) const {
@@ -125,7 +126,7 @@ struct PagedWalk {
   }
   // Interval `cta` of `grid` equal ones of a line of `total` units; false if it is empty.
   DG_HD bool take_interval(long long total, int cta, int grid) {
-    per = lmax(1, (total + grid - 1) / grid);
+    per = lmax(1, total >> 31 ? (total + grid - 1) / grid : (long long)(((unsigned)total + grid - 1u) / (unsigned)grid));
     x = lmin(total, cta * per);
     x1 = lmin(total, x + per);
     return x < x1;
@@ -144,13 +145,56 @@ struct PagedWalk {
     part = 0;
     seq = i;
     s = paged_seq(a.b, i);
+    tile = 0;
+    const int n = tiles_of(s);
+    kvh = 0;
+#ifdef __CUDA_ARCH__
+    // 32 tiles at a time (called by whole warps); every key head has the same tiles
+    const int lane = threadIdx.x & 31;
+    const long long each = warp_units(s);
+    if (a.n_kv_heads > 1 && each > 0) {
+      const long long y = x - x0;
+      kvh = (int)lmin(a.n_kv_heads - 1, y >> 31 ? y / each : (long long)((unsigned)y / (unsigned)lmin(each, 0x7fffffff)));
+    }
+    tile_x0 = x0 + kvh * each;
+    for (int t0 = 0; t0 < n; t0 += 32) {
+      const int len = t0 + lane < n ? kTileCost + tile_blocks(s, 0, t0 + lane) : 0;
+      int incl = len;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, x < tile_x0 + incl);   // the tile of x or a later one
+      const int k = past ? __ffs(past) - 1 : 31;
+      const int before = __shfl_sync(0xffffffffu, incl - len, k), all = __shfl_sync(0xffffffffu, incl, 31);
+      if (past || t0 + 32 >= n) {
+        tile = imin(t0 + k, n - 1);
+        tile_x0 += before;
+        break;
+      }
+      tile_x0 += all;
+    }
+#else
     const long long each = lmax(1, seq_units(s, 0));
     kvh = (int)lmin(a.n_kv_heads - 1, (x - x0) / each);
-    tile = 0;
     tile_x0 = x0 + kvh * each;
-    const int n = tiles_of(s);
     for (int len; tile + 1 < n && x >= tile_x0 + (len = kTileCost + tile_blocks(s, 0, tile)); ++tile) tile_x0 += len;
+#endif
   }
+
+#ifdef __CUDACC__
+  // seq_units(q, 0) by a whole warp, the same q in every lane
+  __device__ long long warp_units(const PagedSeq& q) const {
+    const int n = tiles_of(q);
+    if (!a.causal) return seq_units(q, 0);
+    long long sum = 0;
+    for (int i = threadIdx.x & 31; i < n; i += 32) sum += kTileCost + tile_blocks(q, 0, i);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  }
+#endif
 
   // Finds the CTA's interval and where it starts; called by all kThreads
   // threads of the CTA, which share `tmp` and `found`.  Every thread adds up a
@@ -164,7 +208,19 @@ struct PagedWalk {
     const int run = (b.n_seqs + kThreads - 1) / kThreads;
     const int i0 = min(b.n_seqs, (int)threadIdx.x * run), i1 = min(b.n_seqs, i0 + run);
     long long sum = 0;
-    for (int i = i0; i < i1; ++i) sum += seq_units(paged_seq(b, i), 0);
+    for (int k = 0; k < run; ++k) {
+      PagedSeq q{0, 0, 0};
+      if (i0 + k < i1) q = paged_seq(b, i0 + k);
+      // sequences of many tiles are summed by the warp, one after the other
+      const bool many = a.causal && tiles_of(q) > 2;
+      if (!many) sum += seq_units(q, 0);
+      for (unsigned m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
+        const int l = __ffs(m) - 1;
+        const PagedSeq o{0, __shfl_sync(0xffffffffu, q.nq, l), __shfl_sync(0xffffffffu, q.kv, l)};
+        const long long u = warp_units(o);
+        if (lane == l) sum += u;
+      }
+    }
     sum *= a.n_kv_heads;
     long long incl = sum;
 #pragma unroll
@@ -191,7 +247,7 @@ struct PagedWalk {
     if (y >= incl - sum && y < incl) {
       long long at = incl - sum;
       for (int i = i0; i < i1; ++i) {
-        const long long n = seq_units(paged_seq(b, i), 0) * a.n_kv_heads;
+        const long long n = i1 - i0 == 1 ? sum : seq_units(paged_seq(b, i), 0) * a.n_kv_heads;
         if (y < at + n) {
           found = i;
           tmp[kThreads / 32] = pre + at;
@@ -253,7 +309,7 @@ struct PagedWalk {
         f.whole = f.first && f.nblk == nb;
         // (the CTA of the last block is this one unless the interval ends before it)
         f.n_cont = b0 + nb <= x1 ? 0 : (int)((b0 + nb - 1 - x1) / per) + 1;
-        f.pages = (int)(((long long)f.limit + (1 << a.b.page_shift) - 1) >> a.b.page_shift);
+        f.pages = (int)(((unsigned)f.limit + (1u << a.b.page_shift) - 1) >> a.b.page_shift);
         f.page_list = part == 1 ? a.b.prefix_pages : a.b.table + (long long)seq * a.b.table_stride;
         x += f.nblk;
       }
