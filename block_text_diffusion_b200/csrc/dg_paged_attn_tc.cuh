@@ -28,17 +28,22 @@
 #include "dg_paged_attn.cuh"
 
 constexpr int kPaThreads = 384;
-constexpr int kPaRows = 256, kPaBlk = 128;
+constexpr int kPaBlk = 128;
 constexpr int kPaFrags = 4;       // pieces announced ahead
 constexpr int kPaPart = 96;       // keys of a block whose probabilities go to the MMA before the rest
 constexpr int kPaStage = 4096;    // epilogue staging of a softmax warp: 32 rows x 128 bytes
 
-template <int kHd>
+// kNarrow: tiles of 128 rows, every piece split.  Without the second query
+// tile and the epilogue staging the ring has half as many blocks again, which
+// is what single tokens over long contexts are bound by: the bytes in flight.
+template <int kHd, bool kNarrow>
 struct PaTc {
+  static constexpr int kRows = kNarrow ? 128 : 256;  // of a tile
   static constexpr int kHalves = kHd / 64;           // 128-byte column groups of a row
   static constexpr int kBytes = 128 * kHd * 2;       // 128 rows of Q, K or V
-  static constexpr int kStages = kHd == 128 ? 4 : 8;
-  static constexpr int kSmem = (2 + kStages) * kBytes + 8 * kPaStage + 1024;
+  static constexpr int kStages = (kNarrow ? 6 : 4) * (kHd == 128 ? 1 : 2);
+  static constexpr int kStageBytes = kNarrow ? 0 : 8 * kPaStage;
+  static constexpr int kSmem = (kRows / 128 + kStages) * kBytes + kStageBytes + 1024;
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
@@ -131,16 +136,16 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-template <int kHd>
+template <int kHd, bool kNarrow>
 __global__ void __launch_bounds__(kPaThreads, 1)
 k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const __grid_constant__ PagedAttnArgs a) {
-  using C = PaTc<kHd>;
-  constexpr int ST = C::kStages;
+  using C = PaTc<kHd, kNarrow>;
+  constexpr int ST = C::kStages, kRows = C::kRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;                             // A, B
-  uint8_t* sKV = smem + 2 * C::kBytes;            // ring of K and V blocks
+  uint8_t* sKV = smem + kRows / 128 * C::kBytes;            // ring of K and V blocks
   uint8_t* sStage = sKV + ST * C::kBytes;         // epilogue staging
   __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], frag_full[kPaFrags], frag_empty[kPaFrags];
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], o_done[2], half_full, half_empty, v_last, v_tail[2], turn[2][4];
@@ -174,7 +179,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (warp == 0) tmem_alloc(&tmem_base, 512);
   if (warp == 8 && lane == 0) { prefetch_tmap(&tmK); prefetch_tmap(&tmV); }
   pdl_wait();
-  PagedWalk<kPaRows, kPaBlk> walk(a);
+  PagedWalk<kRows, kPaBlk> walk(a);
   const bool any = walk.template begin<kPaThreads>(s_tmp, s_found);
   tc_fence_before();
   __syncthreads();
@@ -197,7 +202,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         mbar_arrive(&frag_full[slot]);
       }
       if (f.nblk == 0) break;
-      const bool split = f.rows <= 128;
+      const bool split = kNarrow || f.rows <= 128;
       // The page ids of 32 pages are held by the 32 lanes, for K and for V apart
       // (in a split piece V trails K by two blocks).
       int base_k = -64, base_v = -64, id_k = 0, id_v = 0;
@@ -258,7 +263,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!ok) break;
         const PagedFrag& sf = s_frag[fi % kPaFrags];
         const int n = sf.nblk;
-        const bool wide = sf.rows > 128, tail = sf.limit < (sf.kb0 + n) * kPaBlk;
+        const bool wide = !kNarrow && sf.rows > 128, tail = sf.limit < (sf.kb0 + n) * kPaBlk;
         mbar_arrive(&frag_empty[fi % kPaFrags]);
         if (n == 0) break;
         // (both threads follow every phase of q_full[0], needed or not: a parity
@@ -360,7 +365,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       if (n == 0) break;
       blocks += 2 * n;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < kRows / 128; ++t) {
         if (t * 128 >= rows || !ok) continue;   // no B in a split piece
         if (used[t] > 0) ok = pa_wait(&q_empty[t], (used[t] - 1) & 1, err);
         if (!ok) continue;
@@ -390,7 +395,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         fence_async_smem();
         __syncwarp();
-        const bool wide = rows > 128;
+        const bool wide = !kNarrow && rows > 128;
         if (lane == 0) {
           if (wide || ((n - 1) & 1) == 0) mbar_arrive(&v_tail[0]);
           if (wide || ((n - 1) & 1) == 1) mbar_arrive(&v_tail[1]);
@@ -410,7 +415,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       if (!ok) break;
       const PagedFrag& sf = s_frag[fi % kPaFrags];
       const int nblk = sf.nblk, kb0 = sf.kb0, part = sf.part;
-      const bool split = sf.rows <= 128, first = sf.first, whole = sf.whole;
+      const bool split = kNarrow || sf.rows <= 128, first = sf.first, whole = sf.whole;
       const int row_t = split ? r : t * 128 + r;     // row of the tile
       const int n_rows = min(128, sf.rows - (split ? 0 : t * 128));
       const int n_cont = sf.n_cont, rem0 = sf.rem0;
@@ -467,9 +472,12 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
           // The exponential unit is what both softmaxes need most; the warps of A
           // and B on it take turns, so one exponentiates while the other's MMAs run.
-          ok = pa_wait(&turn[t][wt], turn_phase, err);
-          turn_phase ^= 1;
-          if (!ok) break;
+          // (A narrow piece waits for memory, not for exponentials.)
+          if (!kNarrow) {
+            ok = pa_wait(&turn[t][wt], turn_phase, err);
+            turn_phase ^= 1;
+            if (!ok) break;
+          }
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
           // P is rounded to bf16 for the MMA (its operands are 16-bit); the row
           // sum adds the fp32 values
@@ -491,21 +499,23 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               warp_arrive(&p_part[t]);
             }
           }
-          if (lane == 0) mbar_arrive(&turn[1 - t][wt]);
+          if (!kNarrow && lane == 0) mbar_arrive(&turn[1 - t][wt]);
           l_run = l_run * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
           m_run = m_new;
           tmem_wait_st();
         } else {
-          ok = pa_wait(&turn[t][wt], turn_phase, err);
-          turn_phase ^= 1;
-          if (!ok) break;
-          warp_arrive(&turn[1 - t][wt]);
+          if (!kNarrow) {
+            ok = pa_wait(&turn[t][wt], turn_phase, err);
+            turn_phase ^= 1;
+            if (!ok) break;
+            warp_arrive(&turn[1 - t][wt]);
+          }
           warp_arrive(&p_part[t]);
         }
         tc_fence_before();
         warp_arrive(&p_full[t]);
       }
-      if (ok && split && t == 1 && (nblk & 1)) {     // A had one turn more
+      if (!kNarrow && ok && split && t == 1 && (nblk & 1)) {     // A had one turn more
         ok = pa_wait(&turn[1][wt], turn_phase, err);
         turn_phase ^= 1;
         if (ok) warp_arrive(&turn[0][wt]);
@@ -547,8 +557,8 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         char* dst = nullptr;
         if (r < n_rows) {
           if (first)
-            a.meta[part * rows_all + row] = final ? make_int2(-1, 0) : make_int2((int)blockIdx.x, n_cont * kPaRows + row_t);
-          const long long at = first ? part * rows_all + row : (long long)blockIdx.x * kPaRows + row_t;
+            a.meta[part * rows_all + row] = final ? make_int2(-1, 0) : make_int2((int)blockIdx.x, n_cont * kRows + row_t);
+          const long long at = first ? part * rows_all + row : (long long)blockIdx.x * kRows + row_t;
           if (final) {
             dst = (char*)((bf16*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs);
             if (a.lse) a.lse[row] = l2 * kLn2;
@@ -557,63 +567,63 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             (first ? a.part_lse : a.slot_lse)[at] = l2;
           }
         }
-        // 32 rows x 128 bytes at a time through shared memory: a warp then
-        // stores whole 128-byte lines, four rows an instruction (a thread
-        // storing its own row touches 32 lines an instruction)
         uint8_t* stage = sStage + warp * kPaStage;
         const int cols = final ? 64 : 32;            // columns of 128 bytes
         const int live = min(32, n_rows - wt * 32);
         const bool add_b = __any_sync(0xffffffffu, w1 != 0.0f);
 #pragma unroll 1
-        for (int q = 0; q < kHd; q += cols) {
-#pragma unroll 1
-          for (int h = 0; h < cols; h += 32) {
-            uint32_t o[32];
-            tmem_ld32_nw(tO + q + h, o);
+        for (int q = 0; q < kHd; q += 32) {
+          uint32_t o[32];
+          tmem_ld32_nw(tO + q, o);
+          if (add_b) {
+            uint32_t ob[32];
+            tmem_ld32_nw(tO + 128 + q, ob);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const float x = w0 == 0.0f ? 0.0f : __uint_as_float(o[u]) * w0;
+              o[u] = __float_as_uint(w1 == 0.0f ? x : fmaf(__uint_as_float(ob[u]), w1, x));
+            }
+          } else {
             tmem_wait_ld();
 #pragma unroll
             for (int u = 0; u < 32; ++u) o[u] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[u]) * w0);
-            if (add_b) {
-              uint32_t ob[32];
-              tmem_ld32_nw(tO + 128 + q + h, ob);
-              tmem_wait_ld();
-              if (w1 != 0.0f) {
+          }
+          if (final) {
 #pragma unroll
-                for (int u = 0; u < 32; ++u)
-                  o[u] = __float_as_uint(fmaf(__uint_as_float(ob[u]), w1, __uint_as_float(o[u])));
-              }
-            }
-            // 16-byte chunk c of row r at c ^ (r & 7)
-            if (final) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[u * 8 + e]);
-                uint32_t b[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const __nv_bfloat162 pr = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-                  b[e] = *reinterpret_cast<const uint32_t*>(&pr);
-                }
-                *reinterpret_cast<uint4*>(stage + lane * 128 + (((h / 8 + u) ^ (lane & 7)) << 4)) =
-                    make_uint4(b[0], b[1], b[2], b[3]);
-              }
-            } else {
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                    make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
+            for (int u = 0; u < 16; ++u) {
+              const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(o[2 * u]), __uint_as_float(o[2 * u + 1]));
+              o[u] = *reinterpret_cast<const uint32_t*>(&pr);
             }
           }
+          const int chunks = final ? 4 : 8;          // of 16 bytes
+          if (kNarrow) {                             // few rows: each lane stores its own
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (u < chunks && dst)
+                *reinterpret_cast<uint4*>(dst + q * (128 / cols) + u * 16) =
+                    make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
+            continue;
+          }
+          // 32 rows x 128 bytes through shared memory, chunk c of row r at
+          // c ^ (r & 7): a warp then stores whole 128-byte lines, four rows an
+          // instruction (a thread storing its own row touches 32 lines)
+          const int c0 = final ? (q & 32) / 8 : 0;
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (u < chunks)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((c0 + u) ^ (lane & 7)) << 4)) =
+                  make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
+          if (final && (q & 32) == 0) continue;      // the second half of the 128 bytes follows
+          const int at = final ? (q - 32) * 2 : q * 4;
           __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
           for (int i = 0; i < 32; i += 4) {
             if (i >= live) break;
             const int rr = i + (lane >> 3), c = lane & 7;
             char* to = (char*)__shfl_sync(0xffffffffu, (unsigned long long)dst, rr);
             if (to)
-              *reinterpret_cast<uint4*>(to + q * (128 / cols) + c * 16) =
+              *reinterpret_cast<uint4*>(to + at + c * 16) =
                   *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
           }
           __syncwarp();

@@ -179,6 +179,7 @@ dg_status run_head_rows(int dtype, HeadRowsArgs& a, cudaStream_t s) {
 }
 
 // Workspace of the paged attention; every part starts on 256 bytes.
+constexpr int kPaMaxRows = 256;   // rows of the largest tile
 struct PagedSpace {
   size_t meta, part_lse, slot_lse, part_o, slot_o, total;
 };
@@ -193,9 +194,9 @@ PagedSpace paged_space(int64_t n_tokens, int64_t n_heads, int64_t head_dim, bool
   };
   p.meta = take(rows * sizeof(int2));
   p.part_lse = take(rows * 4);
-  p.slot_lse = take((size_t)kSMs * kPaRows * 4);
+  p.slot_lse = take((size_t)kSMs * kPaMaxRows * 4);
   p.part_o = take(rows * head_dim * 4);
-  p.slot_o = take((size_t)kSMs * kPaRows * head_dim * 4);
+  p.slot_o = take((size_t)kSMs * kPaMaxRows * head_dim * 4);
   p.total = at;
   return p;
 }
@@ -209,23 +210,33 @@ dg_status run_join(const PagedAttnArgs& a, int tile, cudaStream_t s) {
   return done(launch(k_paged_join<T, kHd, 1>, blocks, 256, 0, s, a, tile, (int)kSMs));
 }
 
+template <int kHd, bool kNarrow>
+cudaError_t launch_tc(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, cudaStream_t s) {
+  using C = PaTc<kHd, kNarrow>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_paged_attn_tc<kHd, kNarrow>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  return e != cudaSuccess ? e : launch(k_paged_attn_tc<kHd, kNarrow>, kSMs, kPaThreads, C::kSmem, s, tk, tv, a);
+}
+
 template <int kHd>
 dg_status run_paged_attention(const dg_paged_kv* c, PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e;
+  // Tiles of 128 rows where the average sequence has no more (single tokens);
+  // the lengths themselves are on the device.
+  const bool narrow = (long long)a.b.n_tokens * a.G <= 128ll * a.b.n_seqs;
   if (c->dtype == DG_BF16) {
     CUtensorMap tk, tv;
     const long long outer = (long long)c->n_pages * c->n_kv_heads;
     if (!page_map(&tk, c->k, outer, c->page_size, kHd) || !page_map(&tv, c->v, outer, c->page_size, kHd))
       return DG_ERR_CUDA;
-    e = cudaFuncSetAttribute(k_paged_attn_tc<kHd>, cudaFuncAttributeMaxDynamicSharedMemorySize, PaTc<kHd>::kSmem);
-    if (e == cudaSuccess) e = launch(k_paged_attn_tc<kHd>, kSMs, kPaThreads, PaTc<kHd>::kSmem, s, tk, tv, a);
+    e = narrow ? launch_tc<kHd, true>(tk, tv, a, s) : launch_tc<kHd, false>(tk, tv, a, s);
   } else {
     e = cudaFuncSetAttribute(k_paged_attn_f32<kHd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              paged_f32_smem<kHd>());
     if (e == cudaSuccess) e = launch(k_paged_attn_f32<kHd>, kSMs, 256, paged_f32_smem<kHd>(), s, a);
   }
   if (e != cudaSuccess) return done(e);
-  return c->dtype == DG_BF16 ? run_join<bf16, kHd>(a, kPaRows, s) : run_join<float, kHd>(a, kPaF32Rows, s);
+  return c->dtype == DG_BF16 ? run_join<bf16, kHd>(a, narrow ? 128 : 256, s) : run_join<float, kHd>(a, kPaF32Rows, s);
 }
 
 }  // namespace
@@ -331,7 +342,7 @@ extern "C" dg_status dg_test_paged_walk(const dg_paged_kv* cache, const dg_paged
                                         int32_t causal, int32_t tile_rows, int32_t* status_word, int32_t* out,
                                         int32_t cap, int32_t* n_out) {
   if (!cache_ok(cache) || !batch_ok(cache, batch) || n_heads < 1 || n_heads > 32768 || n_heads % cache->n_kv_heads) return DG_ERR_INVALID_ARG;
-  if ((tile_rows != kPaRows && tile_rows != kPaF32Rows) || !out || !n_out) return DG_ERR_INVALID_ARG;
+  if ((tile_rows != 256 && tile_rows != 128 && tile_rows != kPaF32Rows) || !out || !n_out) return DG_ERR_INVALID_ARG;
   PagedAttnArgs a{};
   a.b = device_batch(cache, batch, status_word);
   a.n_heads = n_heads;
@@ -353,7 +364,9 @@ extern "C" dg_status dg_test_paged_walk(const dg_paged_kv* cache, const dg_paged
     }
     return true;
   };
-  const bool ok = tile_rows == kPaRows ? walk(PagedWalk<kPaRows, kPaBlk>(a)) : walk(PagedWalk<kPaF32Rows, kPaF32Blk>(a));
+  const bool ok = tile_rows == 256   ? walk(PagedWalk<256, kPaBlk>(a))
+                  : tile_rows == 128 ? walk(PagedWalk<128, kPaBlk>(a))
+                                     : walk(PagedWalk<kPaF32Rows, kPaF32Blk>(a));
   *n_out = n;
   return ok ? DG_OK : DG_ERR_INVALID_ARG;
 }

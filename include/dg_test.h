@@ -243,8 +243,8 @@ int32_t dg_launches_per_round(const dg_model* model);
 
 /* Host only: the pieces of work dg_paged_attention cuts a batch into.  Every
  * pointer of `batch` is host memory here (the cache's pages are not touched).
- * tile_rows: 256 (bf16 tiles, 128 keys a block) or 64 (fp32 tiles, 64 keys a
- * block).  out: int32 [cap][16] rows of {CTA, part (0 own keys, 1 the prefix),
+ * tile_rows: 256 or 128 (bf16 tiles, 128 keys a block) or 64 (fp32 tiles, 64
+ * keys a block).  out: int32 [cap][16] rows of {CTA, part (0 own keys, 1 the prefix),
  * sequence (-1: the prefix), first token, first row, rows, key head, first key
  * block, key blocks, visible keys of the last row, vis0, vis_max (row r sees
  * the keys below min(vis_max, vis0 + (first row + r) / G)), page list entries,

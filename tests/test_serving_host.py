@@ -221,7 +221,7 @@ def walk(L, cu, kv, max_pages, page, hq, hk, causal, tile, prefix=0, n_tokens=No
 def expected_tiles(cu, kv, hq, hk, causal, tile, prefix):
     """{(part, seq, kvh, row0): (rows, key blocks)} by the definition: a tile
     has the blocks up to the last key its last row sees, and one at least."""
-    blk = 128 if tile == 256 else 64
+    blk = 64 if tile == 64 else 128
     g = hq // hk
     out = {}
     seqs = [(0, b, cu[b + 1] - cu[b], kv[b]) for b in range(len(kv))]
@@ -236,7 +236,7 @@ def expected_tiles(cu, kv, hq, hk, causal, tile, prefix):
     return out
 
 
-@pytest.mark.parametrize("tile", [256, 64])
+@pytest.mark.parametrize("tile", [256, 128, 64])
 def test_walk_covers_every_block_once(L, tile):
     rng = random.Random(tile)
     for _ in range(150):
