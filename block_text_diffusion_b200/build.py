@@ -1,4 +1,5 @@
-"""Compile the CUDA library (libdg.so) in-tree for sm_100a.
+"""Compile the CUDA library (libdg.so) and the serving binding (_serving.so)
+in-tree, for sm_100a.
 
 The shared object is written next to this file; `python -m
 block_text_diffusion_b200.build` rebuilds it when any source is newer.
@@ -14,9 +15,14 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libdg.so")
-SOURCES = sorted(glob.glob(os.path.join(HERE, "csrc", "*"))) + sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
+SOURCES = sorted(glob.glob(os.path.join(HERE, "csrc", "*.cu*")) + glob.glob(os.path.join(HERE, "csrc", "*.inc"))) + sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
 UNITS = ("dg_engine.cu", "dg_noalloc.cu", "dg_serve.cu")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+
+
+# The Python side of the serving operators: C++ against torch's headers.
+BINDING = os.path.join(HERE, "_serving.so")
+BINDING_SOURCES = [os.path.join(HERE, "csrc", "dg_serving_py.cpp"), os.path.join(ROOT, "include", "dg.h")]
 
 
 def nvcc() -> str:
@@ -33,7 +39,29 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in SOURCES)
 
 
+def build_binding(force: bool = False) -> str:
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING)
+                                                     for s in BINDING_SOURCES):
+        return BINDING
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    subprocess.check_call(["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                           *["-I" + d for d in dirs], "-o", tmp, BINDING_SOURCES[0], "-L" + os.path.join(root, "lib"),
+                           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, lib: str = LIB) -> str:
+    if lib == LIB:
+        build_binding(force)
     if not force and lib == LIB and not stale():
         return lib
     tmp = lib + ".tmp%d" % os.getpid()

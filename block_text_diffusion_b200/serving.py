@@ -1,6 +1,7 @@
 """Serving operators over a paged key/value cache (include/dg.h).
 
-Argument checks and marshalling; the work is in libdg.so.  Tensors may be
+Argument checks and marshalling (in C++, csrc/dg_serving_py.cpp: the calls are
+short); the work is in libdg.so.  Tensors may be
 views with any token and head stride as long as the components of a head are
 contiguous.  Every call is asynchronous on `stream` (default: the current
 stream of the tensors' device), allocates nothing but a workspace the caller
@@ -15,8 +16,9 @@ from __future__ import annotations
 
 import ctypes
 import math
-from array import array
+import os
 
+NATIVE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serving.so")
 _I32, _I64, _F, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
 
@@ -54,31 +56,24 @@ def signatures():
     }
 
 
-class _Runtime:
-    """What every call needs, looked up once: a small call takes the GPU a few
-    microseconds, less than the imports and objects of a careless one."""
+_NAMES = ("dg_qk_norm_rope", "dg_paged_append", "dg_paged_attention", "dg_paged_attention_workspace")
+_bound = None
 
-    def __init__(self):
-        import torch
+
+def _native():
+    """The compiled side of this module (csrc/dg_serving_py.cpp), bound to libdg.so."""
+    global _bound
+    if _bound is None:
+        import torch  # noqa: F401  (the module links against it)
 
         import block_text_diffusion_b200 as package
-        lib = package.lib()
-        self.torch, self.DGError, self.check = torch, package.DGError, package._check
-        self.Tensor, self.f32, self.bf16, self.i32 = torch.Tensor, torch.float32, torch.bfloat16, torch.int32
-        self.norm_rope, self.append = lib.dg_qk_norm_rope, lib.dg_paged_append
-        self.attention, self.workspace = lib.dg_paged_attention, lib.dg_paged_attention_workspace
-        self.current_device = torch.cuda.current_device
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-_runtime = None
-
-
-def _rt():
-    global _runtime
-    if _runtime is None:
-        _runtime = _Runtime()
-    return _runtime
+        L = package.lib()
+        if not os.path.exists(NATIVE_PATH):
+            raise RuntimeError(f"{NATIVE_PATH} is missing: build it with `python -m block_text_diffusion_b200.build`")
+        from . import _serving
+        _serving.bind(*[ctypes.cast(getattr(L, n), _P).value for n in _NAMES], package.DGError)
+        _bound = _serving
+    return _bound
 
 
 def _need(ok, what):
@@ -95,28 +90,6 @@ def _tensor(t, name, dtype, dim, device=None, contiguous=False):
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
-
-
-def _rows(rt, t, name, dtype, shape, index):
-    """(address, token stride, head stride) of a [tokens, heads, head_dim] tensor."""
-    if not isinstance(t, rt.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {list(shape)} on cuda:{index}")
-    st, sh, si = t.stride()
-    if si != 1 and shape[2] > 1 and shape[0] * shape[1] > 0:
-        raise ValueError(f"{name}: the components of a head must be contiguous")
-    return t.data_ptr(), st, sh
-
-
-def _out_rows(rt, t, name, dtype, shape, index):
-    """The same for an output, whose rows may not share memory (several warps
-    would write them at once)."""
-    r = _rows(rt, t, name, dtype, shape, index)
-    tokens, heads, dim = shape
-    if not (r[2] >= dim and r[1] >= (heads - 1) * r[2] + dim):
-        (a, na), (b, nb) = sorted([(r[1], tokens), (r[2], heads)])
-        if tokens * heads and ((na > 1 and a < dim) or (nb > 1 and b < (na - 1) * a + dim)):
-            raise ValueError(f"{name}: rows overlap")
-    return r
 
 
 def _dtype_code(dtype):
@@ -152,12 +125,6 @@ class HeadNorm:
         self._c = _HeadNorm(1, float(eps), None if q_gain is None else q_gain.data_ptr(),
                             None if k_gain is None else k_gain.data_ptr())
         self._at = ctypes.addressof(self._c)
-
-    def _check(self, rt, dtype, dim, index):
-        for g in (self.q_gain, self.k_gain):
-            if g is not None and (g.dtype is not dtype or g.shape != (dim,) or g.get_device() != index
-                                  or not g.is_contiguous()):
-                raise ValueError(f"gains must be contiguous {dtype} tensors of {dim} entries on cuda:{index}")
 
 
 def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=None, beta_fast=32.0,
@@ -252,39 +219,11 @@ class PagedBatch:
             _tensor(prefix_pages, "prefix_pages", i32, 1, cu_q.device, contiguous=True)
         self.cu_q, self.kv_lens, self.page_table, self.prefix_pages = cu_q, kv_lens, page_table, prefix_pages
         self.n_seqs, self.prefix_len, self.index = n, int(prefix_len), cu_q.get_device()
-        # dg_paged_batch as 8-byte words, behind the first (n_seqs, n_tokens)
-        self._words = (cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
+        # what dg_paged_batch needs
+        self._words = (self.index, n, cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
                        max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
-                       prefix_pages.data_ptr() if prefix_len else 0, int(prefix_len))
-
-    def _check(self, cache):
-        if self.index != cache.index:
-            raise ValueError("the batch and the cache are on different devices")
-        if self.prefix_len and self.prefix_pages.numel() * cache.page_size < self.prefix_len:
-            raise ValueError("prefix_pages has fewer pages than prefix_len needs")
-
-
-def _launch(rt, index, stream, name, call):
-    """call(stream handle) with the tensors' device current."""
-    if stream is not None and stream.device.index != index:
-        raise ValueError(f"stream must be one of cuda:{index}")
-    if rt.current_device() == index:
-        rt.check(call(rt.raw_stream(index) if stream is None else stream.cuda_stream), name)
-    else:
-        with rt.torch.cuda.device(index):
-            rt.check(call(rt.raw_stream(index) if stream is None else stream.cuda_stream), name)
-
-
-def _status_at(rt, status, index):
-    if status is None:
-        return None
-    if not isinstance(status, rt.Tensor) or status.dtype is not rt.i32 or status.shape != (1,) \
-            or status.get_device() != index:
-        raise ValueError(f"status must be an int32 tensor of one entry on cuda:{index}")
-    return status.data_ptr()
-
-
-_NO_ROWS = (0, 0, 0)
+                       prefix_pages.data_ptr() if prefix_len else 0, int(prefix_len),
+                       prefix_pages.numel() if prefix_len else 0)
 
 
 def qk_norm_rope(q, k, positions, q_out, k_out, rope=None, norm=None, stream=None):
@@ -292,42 +231,7 @@ def qk_norm_rope(q, k, positions, q_out, k_out, rope=None, norm=None, stream=Non
 
     q [T, Hq, hd] -> q_out, k [T, Hkv, hd] -> k_out (a pair may be None;
     outputs may be the inputs), positions int32 [T] (None without rope)."""
-    rt = _rt()
-    x = q if q is not None else k
-    if not isinstance(x, rt.Tensor) or not x.is_cuda or x.dim() != 3:
-        raise ValueError("q or k must be a 3-D tensor on a GPU")
-    dtype, (tokens, _, dim), index = x.dtype, x.shape, x.get_device()
-    code = 1 if dtype is rt.bf16 else _dtype_code(dtype)
-    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
-        raise ValueError("q and q_out, k and k_out go together")
-    hq = hk = 0
-    qr = qo = kr = ko = _NO_ROWS
-    if q is not None:
-        hq = q.shape[1]
-        shape = (tokens, hq, dim)
-        qr, qo = _rows(rt, q, "q", dtype, shape, index), _out_rows(rt, q_out, "q_out", dtype, shape, index)
-    if k is not None:
-        hk = k.shape[1] if k.dim() == 3 else 0
-        shape = (tokens, hk, dim)
-        kr, ko = _rows(rt, k, "k", dtype, shape, index), _out_rows(rt, k_out, "k_out", dtype, shape, index)
-    at = None
-    if positions is not None:
-        if not isinstance(positions, rt.Tensor) or positions.dtype is not rt.i32 or positions.shape != (tokens,) \
-                or positions.get_device() != index or not positions.is_contiguous():
-            raise ValueError(f"positions must be a contiguous int32 tensor of {tokens} entries on cuda:{index}")
-        at = positions.data_ptr()
-    if rope is not None:
-        if at is None:
-            raise ValueError("rope needs positions")
-        if rope.index != index:
-            raise ValueError(f"inv_freq must be on cuda:{index}")
-    if norm is not None:
-        norm._check(rt, dtype, dim, index)
-    args = array("q", (*qr, *qo, *kr, *ko))
-    p = args.buffer_info()[0]
-    _launch(rt, index, stream, "dg_qk_norm_rope", lambda s: rt.norm_rope(
-        code, tokens, hq, hk, dim, p, p + 24, p + 48, p + 72, at, None if rope is None else rope._at,
-        None if norm is None else norm._at, s))
+    _native().qk_norm_rope(q, k, positions, q_out, k_out, rope, norm, stream)
 
 
 def paged_append(cache, batch, k, v, rope=None, norm=None, q=None, q_out=None, status=None, stream=None):
@@ -337,36 +241,15 @@ def paged_append(cache, batch, k, v, rope=None, norm=None, q=None, q_out=None, s
 
     status: int32 [1] device tensor, zero before; becomes 5 (DG_ERR_STATE) if a
     token had no valid slot (it is not stored)."""
-    rt = _rt()
-    if not isinstance(k, rt.Tensor) or k.dim() != 3 or (q is None) != (q_out is None):
-        raise ValueError("k must be a 3-D tensor, and q and q_out go together")
-    dtype, index, dim, tokens = cache.dtype, cache.index, cache.head_dim, k.shape[0]
-    shape = (tokens, cache.n_kv_heads, dim)
-    kr, vr = _rows(rt, k, "k", dtype, shape, index), _rows(rt, v, "v", dtype, shape, index)
-    hq, qr, qo = 0, _NO_ROWS, _NO_ROWS
-    if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        shape = (tokens, hq, dim)
-        qr, qo = _rows(rt, q, "q", dtype, shape, index), _out_rows(rt, q_out, "q_out", dtype, shape, index)
-    if rope is not None and rope.index != index:
-        raise ValueError(f"inv_freq must be on cuda:{index}")
-    if norm is not None:
-        norm._check(rt, dtype, dim, index)
-    batch._check(cache)
-    args = array("q", (*kr, *vr, *qr, *qo, batch.n_seqs | tokens << 32, *batch._words))
-    p = args.buffer_info()[0]
-    word = _status_at(rt, status, index)
-    _launch(rt, index, stream, "dg_paged_append", lambda s: rt.append(
-        cache._at, p + 96, p, p + 24, None if rope is None else rope._at, None if norm is None else norm._at, hq,
-        p + 48, p + 72, word, s))
+    _native().paged_append(cache, batch, k, v, rope, norm, q, q_out, status, stream)
 
 
 def paged_attention_workspace(n_tokens, n_heads, head_dim, with_prefix=False):
     """Bytes of workspace paged_attention needs for that many token rows."""
-    rt = _rt()
-    n = int(rt.workspace(n_tokens, n_heads, head_dim, int(bool(with_prefix))))
+    from . import DGError, lib
+    n = int(lib().dg_paged_attention_workspace(n_tokens, n_heads, head_dim, int(bool(with_prefix))))
     if n == 0:
-        raise rt.DGError(1, "dg_paged_attention_workspace")
+        raise DGError(1, "dg_paged_attention_workspace")
     return n
 
 
@@ -381,34 +264,17 @@ def paged_attention(cache, batch, q, out, scale=None, causal=True, lse=None, wor
     paged_attention_workspace(...) bytes (None: allocated for the call); two
     calls that may overlap need two.  status: int32 [1], zero before; becomes 5
     (DG_ERR_STATE) if a page id or length was out of range."""
-    rt = _rt()
-    if not isinstance(q, rt.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a 3-D tensor")
-    tokens, hq, _ = q.shape
-    dtype, index, dim = cache.dtype, cache.index, cache.head_dim
-    shape = (tokens, hq, dim)
-    qr, o = _rows(rt, q, "q", dtype, shape, index), _out_rows(rt, out, "out", dtype, shape, index)
-    if hq < 1 or hq % cache.n_kv_heads:
-        raise ValueError(f"{hq} query heads over {cache.n_kv_heads} key heads")
-    lse_at = None
-    if lse is not None:
-        if not isinstance(lse, rt.Tensor) or lse.dtype is not rt.f32 or lse.shape != (tokens, hq) \
-                or lse.get_device() != index or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 tensor [{tokens}, {hq}] on cuda:{index}")
-        lse_at = lse.data_ptr()
-    batch._check(cache)
+    call = _native().paged_attention
     if workspace is None:
-        s = stream if stream is not None else rt.torch.cuda.current_stream(index)
-        with rt.torch.cuda.stream(s):   # freed, the memory goes back to this stream's pool
-            workspace = rt.torch.empty(paged_attention_workspace(tokens, hq, dim, batch.prefix_len > 0),
-                                       dtype=rt.torch.uint8, device=cache.device)
-    elif not isinstance(workspace, rt.Tensor) or workspace.dtype is not rt.torch.uint8 or workspace.dim() != 1 \
-            or workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous 1-D uint8 tensor on cuda:{index}")
-    args = array("q", (*qr, *o, batch.n_seqs | tokens << 32, *batch._words))
-    p = args.buffer_info()[0]
-    word = _status_at(rt, status, index)
-    scale = dim ** -0.5 if scale is None else scale
-    _launch(rt, index, stream, "dg_paged_attention", lambda s: rt.attention(
-        cache._at, p + 48, hq, p, scale, 1 if causal else 0, p + 24, lse_at, workspace.data_ptr(),
-        workspace.numel(), word, s))
+        import torch
+
+        from . import DGError
+        n = call(cache, batch, q, out, scale, causal, lse, None, status, stream)
+        if n == 0:
+            raise DGError(1, "dg_paged_attention_workspace")
+        if stream is not None and stream.device != cache.device:
+            raise ValueError(f"stream must be one of {cache.device}")
+        # allocated on the call's stream: freed, the memory goes back to that stream's pool
+        with torch.cuda.stream(torch.cuda.current_stream(cache.device) if stream is None else stream):
+            workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
+    call(cache, batch, q, out, scale, causal, lse, workspace, status, stream)
