@@ -83,18 +83,19 @@ constexpr int kTileCost = 2;
 template <int kRows, int kBlk>
 struct PagedWalk {
   const PagedAttnArgs& a;
-  long long x, x1;          // interval left: [x, x1)
-  long long per;            // interval length
+  // (the host refuses batches whose line could reach 2^31 units)
+  int x, x1;          // interval left: [x, x1)
+  int per;            // interval length
   // current tile
-  int part, seq, kvh, tile;
-  long long tile_x0;        // where the current tile starts on the line
-  PagedSeq s;               // the sequence (part 1: the whole batch over the prefix)
+  int part, seq, kvh, tile, n_tiles;
+  int tile_x0;        // where the current tile starts on the line
+  PagedSeq s;         // the sequence (part 1: the whole batch over the prefix)
 
   DG_HD PagedWalk(const PagedAttnArgs& a_) : a(a_) {}
 
-  // (rows of a sequence are at most n_tokens * n_heads < 2^31: 32-bit arithmetic)
+  // (rows of a sequence are at most n_tokens * n_heads < 2^31)
   DG_HD int tiles_of(const PagedSeq& q) const { return (int)(((unsigned)(q.nq * a.G) + kRows - 1) / kRows); }
-  // keys visible to the last row of a tile of the current sequence
+  // keys visible to the last row of a tile
   DG_HD int tile_limit(const PagedSeq& q, int part_, int tl) const {
     if (part_ == 1 || !a.causal) return q.kv;
     const unsigned rows = (unsigned)(q.nq * a.G), end = (unsigned)(tl + 1) * kRows;
@@ -104,61 +105,71 @@ struct PagedWalk {
   DG_HD int tile_blocks(const PagedSeq& q, int part_, int tl) const {
     return imax(1, (int)(((unsigned)tile_limit(q, part_, tl) + kBlk - 1) / kBlk));
   }
-  // units of all tiles of one sequence for one key head
-  DG_HD long long seq_units(const PagedSeq& q, int part_) const {
-    const int n = tiles_of(q);
-    if (part_ == 1 || !a.causal) return (long long)n * (kTileCost + tile_blocks(q, part_, 0));
-    long long sum = 0;
-    for (int i = 0; i < n; ++i) sum += kTileCost + tile_blocks(q, part_, i);
-    return sum;
-  }
+  DG_HD int tile_units(const PagedSeq& q, int part_, int tl) const { return kTileCost + tile_blocks(q, part_, tl); }
   DG_HD PagedSeq whole_batch() const {
     const PagedBatch& b = a.b;
     PagedSeq p;
-    const int lo = b.n_seqs > 0 ? b.cu_q[0] : 0, hi = b.n_seqs > 0 ? b.cu_q[b.n_seqs] : 0;
+    const int lo = b.cu_q[0], hi = b.cu_q[b.n_seqs];
     p.q0 = imin(imax(lo, 0), b.n_tokens);
     p.nq = imin(imax(hi, p.q0), b.n_tokens) - p.q0;
     p.kv = b.prefix_len;
     return p;
   }
-  DG_HD long long prefix_units() const {
-    return a.b.prefix_len > 0 ? seq_units(whole_batch(), 1) * a.n_kv_heads : 0;
+  // units of the tiles of one sequence for one key head (a whole warp asks for one sequence)
+  DG_HD long long units_of(const PagedSeq& q, int part_) const {
+    const int n = tiles_of(q);
+    if (part_ == 1 || !a.causal || n < 2) return n == 0 ? 0 : (long long)n * tile_units(q, part_, 0);
+    long long sum = 0;
+#ifdef __CUDA_ARCH__
+    for (int i = threadIdx.x & 31; i < n; i += 32) sum += tile_units(q, 0, i);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#else
+    for (int i = 0; i < n; ++i) sum += tile_units(q, 0, i);
+#endif
+    return sum;
   }
   // Interval `cta` of `grid` equal ones of a line of `total` units; false if it is empty.
   DG_HD bool take_interval(long long total, int cta, int grid) {
-    per = lmax(1, total >> 31 ? (total + grid - 1) / grid : (long long)(((unsigned)total + grid - 1u) / (unsigned)grid));
-    x = lmin(total, cta * per);
-    x1 = lmin(total, x + per);
+    if (total >> 31) {   // (offsets that overlap)
+      paged_error(a.b, kStatusState);
+      return false;
+    }
+    per = imax(1, (int)(((unsigned)total + grid - 1u) / (unsigned)grid));
+    x = (int)lmin(total, (long long)cta * per);
+    x1 = (int)lmin(total, (long long)x + per);
     return x < x1;
   }
-  DG_HD void enter_prefix() {
+  DG_HD void enter_prefix(int each) {
     part = 1;
     seq = -1;
     s = whole_batch();
-    const long long each = seq_units(s, 1), len = kTileCost + tile_blocks(s, 1, 0);
-    kvh = (int)(x / each);
-    tile = (int)(x % each / len);
+    n_tiles = tiles_of(s);
+    const int len = tile_units(s, 1, 0);
+    kvh = x / each;
+    tile = (x - kvh * each) / len;
     tile_x0 = kvh * each + tile * len;
   }
-  // x lies in sequence i, which starts at x0 on the line
-  DG_HD void enter_sequence(int i, long long x0) {
+  // x lies in sequence i, which starts at x0 on the line (a whole warp)
+  DG_HD void enter_sequence(int i, int x0) {
     part = 0;
     seq = i;
     s = paged_seq(a.b, i);
+    n_tiles = tiles_of(s);
     tile = 0;
-    const int n = tiles_of(s);
-    kvh = 0;
-#ifdef __CUDA_ARCH__
-    // 32 tiles at a time (called by whole warps); every key head has the same tiles
-    const int lane = threadIdx.x & 31;
-    const long long each = warp_units(s);
-    if (a.n_kv_heads > 1 && each > 0) {
-      const long long y = x - x0;
-      kvh = (int)lmin(a.n_kv_heads - 1, y >> 31 ? y / each : (long long)((unsigned)y / (unsigned)lmin(each, 0x7fffffff)));
-    }
+    const int each = imax(1, (int)units_of(s, 0));
+    kvh = imin(a.n_kv_heads - 1, (x - x0) / each);
     tile_x0 = x0 + kvh * each;
-    for (int t0 = 0; t0 < n; t0 += 32) {
-      const int len = t0 + lane < n ? kTileCost + tile_blocks(s, 0, t0 + lane) : 0;
+    if (!a.causal) {   // tiles of one length
+      const int len = tile_units(s, 0, 0);
+      tile = imin(n_tiles - 1, (x - tile_x0) / len);
+      tile_x0 += tile * len;
+      return;
+    }
+#ifdef __CUDA_ARCH__
+    const int lane = threadIdx.x & 31;
+    for (int t0 = 0; t0 < n_tiles; t0 += 32) {   // 32 tiles at a time
+      const int len = t0 + lane < n_tiles ? tile_units(s, 0, t0 + lane) : 0;
       int incl = len;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -168,113 +179,89 @@ struct PagedWalk {
       const unsigned past = __ballot_sync(0xffffffffu, x < tile_x0 + incl);   // the tile of x or a later one
       const int k = past ? __ffs(past) - 1 : 31;
       const int before = __shfl_sync(0xffffffffu, incl - len, k), all = __shfl_sync(0xffffffffu, incl, 31);
-      if (past || t0 + 32 >= n) {
-        tile = imin(t0 + k, n - 1);
+      if (past || t0 + 32 >= n_tiles) {
+        tile = imin(t0 + k, n_tiles - 1);
         tile_x0 += before;
         break;
       }
       tile_x0 += all;
     }
 #else
-    const long long each = lmax(1, seq_units(s, 0));
-    kvh = (int)lmin(a.n_kv_heads - 1, (x - x0) / each);
-    tile_x0 = x0 + kvh * each;
-    for (int len; tile + 1 < n && x >= tile_x0 + (len = kTileCost + tile_blocks(s, 0, tile)); ++tile) tile_x0 += len;
+    for (int len; tile + 1 < n_tiles && x >= tile_x0 + (len = tile_units(s, 0, tile)); ++tile) tile_x0 += len;
 #endif
   }
 
 #ifdef __CUDACC__
-  // seq_units(q, 0) by a whole warp, the same q in every lane
-  __device__ long long warp_units(const PagedSeq& q) const {
+  // Units of sequence base + lane, for all key heads (0 past the last).
+  __device__ __noinline__ long long lane_units(int base) const {
+    const int lane = threadIdx.x & 31;
+    PagedSeq q{0, 0, 0};
+    if (base + lane < a.b.n_seqs) q = paged_seq(a.b, base + lane);
+    // one tile, or tiles of one length: by the lane; the others by the warp
     const int n = tiles_of(q);
-    if (!a.causal) return seq_units(q, 0);
-    long long sum = 0;
-    for (int i = threadIdx.x & 31; i < n; i += 32) sum += kTileCost + tile_blocks(q, 0, i);
+    const bool many = a.causal && n > 1;
+    long long u = n == 0 || many ? 0 : (long long)n * tile_units(q, 0, 0);
+    for (unsigned m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
+      const int l = __ffs(m) - 1;
+      const long long v = units_of(PagedSeq{0, __shfl_sync(0xffffffffu, q.nq, l), __shfl_sync(0xffffffffu, q.kv, l)}, 0);
+      if (lane == l) u = v;
+    }
+    return u * a.n_kv_heads;
+  }
+
+  // Finds the CTA's interval and where it starts, by one warp; false if there
+  // is nothing to do.
+  __device__ bool begin() {
+    const int lane = threadIdx.x & 31, n = a.b.n_seqs;
+    long long mine = 0;
+#pragma unroll 1
+    for (int base = 0; base < n; base += 32) mine += lane_units(base);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    long long each = 0;
+    if (a.b.prefix_len > 0) each = units_of(whole_batch(), 1);
+    const long long pre = each * a.n_kv_heads;
+    if (!take_interval(mine + pre, blockIdx.x, gridDim.x)) return false;
+    if (x < pre) {
+      enter_prefix((int)each);
+      return true;
+    }
+    int at = (int)pre;
+#pragma unroll 1
+    for (int base = 0; base < n; base += 32) {
+      const int len = (int)lane_units(base);
+      int incl = len;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, x < at + incl);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        enter_sequence(base + k, at + __shfl_sync(0xffffffffu, incl - len, k));
+        return true;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;   // (lengths that change while the kernel runs)
   }
 #endif
 
-  // Finds the CTA's interval and where it starts; called by all kThreads
-  // threads of the CTA, which share `tmp` and `found`.  Every thread adds up a
-  // run of sequences and the runs are scanned, so the lengths are read once
-  // per CTA.  False (for every thread): there is nothing to do.
-  template <int kThreads>
-  __device__ bool begin(long long (&tmp)[kThreads / 32 + 1], int& found) {
-    const PagedBatch& b = a.b;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long pre = prefix_units();
-    const int run = (b.n_seqs + kThreads - 1) / kThreads;
-    const int i0 = min(b.n_seqs, (int)threadIdx.x * run), i1 = min(b.n_seqs, i0 + run);
-    long long sum = 0;
-    for (int k = 0; k < run; ++k) {
-      PagedSeq q{0, 0, 0};
-      if (i0 + k < i1) q = paged_seq(b, i0 + k);
-      // sequences of many tiles are summed by the warp, one after the other
-      const bool many = a.causal && tiles_of(q) > 2;
-      if (!many) sum += seq_units(q, 0);
-      for (unsigned m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
-        const int l = __ffs(m) - 1;
-        const PagedSeq o{0, __shfl_sync(0xffffffffu, q.nq, l), __shfl_sync(0xffffffffu, q.kv, l)};
-        const long long u = warp_units(o);
-        if (lane == l) sum += u;
-      }
-    }
-    sum *= a.n_kv_heads;
-    long long incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) tmp[warp] = incl;
-    if (threadIdx.x == 0) found = -1;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += tmp[i];
-      total += tmp[i];
-    }
-    incl += before;
-    if (!take_interval(total + pre, blockIdx.x, gridDim.x)) return false;
-    if (x < pre) {
-      enter_prefix();
-      return true;
-    }
-    // the thread whose run holds x names the sequence and where it starts
-    const long long y = x - pre;
-    if (y >= incl - sum && y < incl) {
-      long long at = incl - sum;
-      for (int i = i0; i < i1; ++i) {
-        const long long n = i1 - i0 == 1 ? sum : seq_units(paged_seq(b, i), 0) * a.n_kv_heads;
-        if (y < at + n) {
-          found = i;
-          tmp[kThreads / 32] = pre + at;
-          break;
-        }
-        at += n;
-      }
-    }
-    __syncthreads();
-    if (found < 0) return false;   // (lengths that change while the kernel runs)
-    enter_sequence(found, tmp[kThreads / 32]);
-    return true;
-  }
-
   // The same on the host, for a batch in host memory.
   bool begin_host(int cta, int grid) {
-    const long long pre = prefix_units();
+    const long long each = a.b.prefix_len > 0 && a.b.n_seqs > 0 ? units_of(whole_batch(), 1) : 0;
+    const long long pre = each * a.n_kv_heads;
     long long total = pre;
-    for (int i = 0; i < a.b.n_seqs; ++i) total += seq_units(paged_seq(a.b, i), 0) * a.n_kv_heads;
+    for (int i = 0; i < a.b.n_seqs; ++i) total += units_of(paged_seq(a.b, i), 0) * a.n_kv_heads;
     if (!take_interval(total, cta, grid)) return false;
     if (x < pre) {
-      enter_prefix();
+      enter_prefix((int)each);
       return true;
     }
-    long long at = pre;
+    int at = (int)pre;
     for (int i = 0; i < a.b.n_seqs; ++i) {
-      const long long n = seq_units(paged_seq(a.b, i), 0) * a.n_kv_heads;
+      const int n = (int)units_of(paged_seq(a.b, i), 0) * a.n_kv_heads;
       if (x < at + n) {
         enter_sequence(i, at);
         return true;
@@ -289,33 +276,33 @@ struct PagedWalk {
     PagedFrag f;
     f.nblk = 0;
     while (x < x1) {
-      const int nb = tile_blocks(s, part, tile);
-      const long long b0 = tile_x0 + kTileCost;   // where block 0 lies
-      x = lmax(x, b0);
+      f.limit = tile_limit(s, part, tile);
+      const int nb = imax(1, (int)(((unsigned)f.limit + kBlk - 1) / kBlk));
+      const int b0 = tile_x0 + kTileCost;   // where block 0 lies
+      x = imax(x, b0);
       if (x < x1) {
         f.part = part;
         f.q0 = s.q0;
         f.row0 = tile * kRows;
-        f.rows = (int)lmin(kRows, (long long)s.nq * a.G - f.row0);
-        f.tok0 = f.row0 / a.G;
+        f.rows = imin(kRows, s.nq * a.G - f.row0);
+        f.tok0 = (int)((unsigned)f.row0 / (unsigned)a.G);
         f.rem0 = f.row0 - f.tok0 * a.G;
         f.kvh = kvh;
-        f.kb0 = (int)lmin(nb - 1, x - b0);
-        f.nblk = (int)lmax(1, lmin(nb - f.kb0, x1 - x));
-        f.limit = tile_limit(s, part, tile);
+        f.kb0 = imin(nb - 1, x - b0);
+        f.nblk = imax(1, imin(nb - f.kb0, x1 - x));
         f.vis_max = s.kv;
         f.vis0 = part == 1 || !a.causal ? s.kv : s.kv - s.nq + 1;
         f.first = f.kb0 == 0;
         f.whole = f.first && f.nblk == nb;
         // (the CTA of the last block is this one unless the interval ends before it)
-        f.n_cont = b0 + nb <= x1 ? 0 : (int)((b0 + nb - 1 - x1) / per) + 1;
+        f.n_cont = b0 + nb <= x1 ? 0 : (b0 + nb - 1 - x1) / per + 1;
         f.pages = (int)(((unsigned)f.limit + (1u << a.b.page_shift) - 1) >> a.b.page_shift);
         f.page_list = part == 1 ? a.b.prefix_pages : a.b.table + (long long)seq * a.b.table_stride;
         x += f.nblk;
       }
       if (x < x1) {   // on to the next tile
         tile_x0 = b0 + nb;
-        if (++tile >= tiles_of(s)) {
+        if (++tile >= n_tiles) {
           tile = 0;
           if (++kvh >= a.n_kv_heads) {
             kvh = 0;
@@ -327,6 +314,7 @@ struct PagedWalk {
               }
               s = paged_seq(a.b, seq);
             } while (s.nq == 0);
+            n_tiles = tiles_of(s);
           }
         }
       }
@@ -489,11 +477,9 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(PagedAttnArgs a) {
   float* sK = sQ + R * kLd;
   float* sV = sK + B * kLd;
   float* sP = sV + B * kHd;
-  __shared__ long long s_tmp[256 / 32 + 1];
-  __shared__ int s_found;
   pdl_enter();
   PagedWalk<R, B> walk(a);
-  if (!walk.template begin<256>(s_tmp, s_found)) return;
+  if (!walk.begin()) return;   // (each warp finds the same)
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   for (;;) {
     const PagedFrag f = walk.next();

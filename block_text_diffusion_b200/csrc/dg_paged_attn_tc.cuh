@@ -151,8 +151,6 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], o_done[2], half_full, half_empty, v_last, v_tail[2], turn[2][4];
   __shared__ PagedFrag s_frag[kPaFrags];
   __shared__ float s_half[128][2];                // split: maximum and sum of B's half, per row
-  __shared__ long long s_tmp[kPaThreads / 32 + 1];
-  __shared__ int s_found;
   __shared__ uint32_t tmem_base;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -179,19 +177,20 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   if (warp == 0) tmem_alloc(&tmem_base, 512);
   if (warp == 8 && lane == 0) { prefetch_tmap(&tmK); prefetch_tmap(&tmV); }
   pdl_wait();
-  PagedWalk<kRows, kPaBlk> walk(a);
-  const bool any = walk.template begin<kPaThreads>(s_tmp, s_found);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  bool ok = any;
+  bool ok = true;
 
   if (warp == 8) {
     // ---------------- walk and TMA ----------------
     const int page_shift = a.b.page_shift, page = 1 << page_shift;
     const int per_blk = page >= kPaBlk ? 1 : kPaBlk >> page_shift;   // pages a block
     int cnt = 0;
+    PagedWalk<kRows, kPaBlk> walk(a);
+    if (!walk.begin()) walk.x = walk.x1 = 0;
+#pragma unroll 1
     for (int fi = 0; ok; ++fi) {
       const PagedFrag f = walk.next();
       const int slot = fi % kPaFrags;
@@ -352,7 +351,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     constexpr int kPer = kHd / 8, kAt = 32 / kPer;   // chunks a row, rows a pass of the warp
     const int c = lane % kPer;
     const uint32_t dst = smem_u32(sQ) + (c >> 3) * 16384;
-    int used[2] = {0, 0}, blocks = 0, tails = 0;     // pieces loaded for; K and V blocks up to this piece; tails cleared
+    int used_a = 0, used_b = 0, blocks = 0, tails = 0;   // pieces loaded for; K and V blocks up to this piece; tails cleared
     for (int fi = 0; ok; ++fi) {
       ok = pa_wait(&frag_full[fi % kPaFrags], (fi / kPaFrags) & 1, err);
       if (!ok) break;
@@ -364,12 +363,12 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       warp_arrive(&frag_empty[fi % kPaFrags]);
       if (n == 0) break;
       blocks += 2 * n;
-#pragma unroll
-      for (int t = 0; t < kRows / 128; ++t) {
-        if (t * 128 >= rows || !ok) continue;   // no B in a split piece
-        if (used[t] > 0) ok = pa_wait(&q_empty[t], (used[t] - 1) & 1, err);
-        if (!ok) continue;
-        ++used[t];
+#pragma unroll 1
+      for (int t = 0; t < kRows / 128 && t * 128 < rows && ok; ++t) {   // (no B in a split piece)
+        int& used = t ? used_b : used_a;
+        if (used > 0) ok = pa_wait(&q_empty[t], (used - 1) & 1, err);
+        if (!ok) break;
+        ++used;
         const int last = min(rows, t * 128 + 128);
 #pragma unroll 4
         for (int row = t * 128 + lane / kPer; row < last; row += kAt) {
@@ -572,34 +571,34 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int live = min(32, n_rows - wt * 32);
         const bool add_b = __any_sync(0xffffffffu, w1 != 0.0f);
 #pragma unroll 1
-        for (int q = 0; q < kHd; q += 32) {
-          uint32_t o[32];
-          tmem_ld32_nw(tO + q, o);
+        for (int q = 0; q < kHd; q += 16) {
+          uint32_t o[16];
+          tmem_ld16_nw(tO + q, o);
           if (add_b) {
-            uint32_t ob[32];
-            tmem_ld32_nw(tO + 128 + q, ob);
+            uint32_t ob[16];
+            tmem_ld16_nw(tO + 128 + q, ob);
             tmem_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
+            for (int u = 0; u < 16; ++u) {
               const float x = w0 == 0.0f ? 0.0f : __uint_as_float(o[u]) * w0;
               o[u] = __float_as_uint(w1 == 0.0f ? x : fmaf(__uint_as_float(ob[u]), w1, x));
             }
           } else {
             tmem_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[u]) * w0);
+            for (int u = 0; u < 16; ++u) o[u] = w0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[u]) * w0);
           }
           if (final) {
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
+            for (int u = 0; u < 8; ++u) {
               const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(o[2 * u]), __uint_as_float(o[2 * u + 1]));
               o[u] = *reinterpret_cast<const uint32_t*>(&pr);
             }
           }
-          const int chunks = final ? 4 : 8;          // of 16 bytes
+          const int chunks = final ? 2 : 4;          // of 16 bytes
           if (kNarrow) {                             // few rows: each lane stores its own
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+            for (int u = 0; u < 4; ++u)
               if (u < chunks && dst)
                 *reinterpret_cast<uint4*>(dst + q * (128 / cols) + u * 16) =
                     make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
@@ -608,14 +607,14 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           // 32 rows x 128 bytes through shared memory, chunk c of row r at
           // c ^ (r & 7): a warp then stores whole 128-byte lines, four rows an
           // instruction (a thread storing its own row touches 32 lines)
-          const int c0 = final ? (q & 32) / 8 : 0;
+          const int c0 = final ? (q & 48) / 8 : (q & 16) / 4;
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
+          for (int u = 0; u < 4; ++u)
             if (u < chunks)
               *reinterpret_cast<uint4*>(stage + lane * 128 + (((c0 + u) ^ (lane & 7)) << 4)) =
                   make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
-          if (final && (q & 32) == 0) continue;      // the second half of the 128 bytes follows
-          const int at = final ? (q - 32) * 2 : q * 4;
+          if ((q + 16) % cols) continue;             // the rest of the 128 bytes follows
+          const int at = (q + 16 - cols) * (128 / cols);
           __syncwarp();
 #pragma unroll 4
           for (int i = 0; i < 32; i += 4) {

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <utility>
 
 #include "../../include/dg.h"
@@ -58,6 +59,20 @@ cudaError_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, size
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The dynamic shared memory of a kernel, raised once on each device (the
+// attribute stays; two threads that raise it at once set the same value).
+template <typename K>
+cudaError_t raise_smem(K kernel, int bytes, std::atomic<uint64_t>& done_on) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done_on.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (r == cudaSuccess) done_on.fetch_or(bit, std::memory_order_release);
+  return r;
 }
 
 dg_status done(cudaError_t e) {
@@ -213,8 +228,8 @@ dg_status run_join(const PagedAttnArgs& a, int tile, cudaStream_t s) {
 template <int kHd, bool kNarrow>
 cudaError_t launch_tc(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a, cudaStream_t s) {
   using C = PaTc<kHd, kNarrow>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_paged_attn_tc<kHd, kNarrow>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> raised{0};
+  const cudaError_t e = raise_smem(k_paged_attn_tc<kHd, kNarrow>, C::kSmem, raised);
   return e != cudaSuccess ? e : launch(k_paged_attn_tc<kHd, kNarrow>, kSMs, kPaThreads, C::kSmem, s, tk, tv, a);
 }
 
@@ -231,8 +246,8 @@ dg_status run_paged_attention(const dg_paged_kv* c, PagedAttnArgs& a, cudaStream
       return DG_ERR_CUDA;
     e = narrow ? launch_tc<kHd, true>(tk, tv, a, s) : launch_tc<kHd, false>(tk, tv, a, s);
   } else {
-    e = cudaFuncSetAttribute(k_paged_attn_f32<kHd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             paged_f32_smem<kHd>());
+    static std::atomic<uint64_t> raised{0};
+    e = raise_smem(k_paged_attn_f32<kHd>, paged_f32_smem<kHd>(), raised);
     if (e == cudaSuccess) e = launch(k_paged_attn_f32<kHd>, kSMs, 256, paged_f32_smem<kHd>(), s, a);
   }
   if (e != cudaSuccess) return done(e);
@@ -310,6 +325,13 @@ extern "C" dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged
   for (const dg_heads* h : {q, out})
     if (!heads_ok(h) || !aligned(h->data, 16) || h->token_stride % per16 || h->head_stride % per16)
       return DG_ERR_INVALID_ARG;
+  // The line of work units (see dg_paged_attn.cuh) is counted in 32 bits: at
+  // most this many tiles of 64 rows, each with every block of 64 keys.
+  const int64_t rows = (int64_t)batch->n_tokens * (n_heads / cache->n_kv_heads);
+  const int64_t keys = (int64_t)batch->max_pages * cache->page_size;
+  if (((rows / 64 + batch->n_seqs) * (keys / 64 + 4) + (rows / 64 + 1) * ((int64_t)batch->prefix_len / 64 + 4)) *
+          cache->n_kv_heads >= (int64_t)1 << 31)
+    return DG_ERR_UNSUPPORTED;
   const PagedSpace sp = paged_space(batch->n_tokens, n_heads, hd, batch->prefix_len > 0);
   char* ws = (char*)workspace;
   PagedAttnArgs a{};

@@ -310,7 +310,10 @@ size_t dg_paged_attention_workspace(int32_t n_tokens, int32_t n_heads, int32_t h
  * n_heads], or NULL) = ln(sum(exp(scores))).  A query that sees no key gets zeros
  * and lse = -inf.  The prefix is read once for the whole batch, not once for
  * each sequence.  head_dim 64 or 128; q and out 16-byte aligned with strides of a
- * multiple of 16 bytes; scale > 0; n_heads a multiple of the cache's n_kv_heads.
+ * multiple of 16 bytes; scale > 0; n_heads a multiple of the cache's n_kv_heads,
+ * at most 32768.  DG_ERR_UNSUPPORTED for another head_dim, and for a batch whose
+ * (rows of a key head / 64 + n_seqs) (max_pages page_size / 64) n_kv_heads, plus
+ * the same for the prefix, reaches 2^31 (about 10^6 tokens over 10^6 keys).
  * Memory in the cache past a sequence's length may hold anything; keys and values
  * within it must be finite.  workspace: device, 256-byte aligned, contents
  * arbitrary, not shared with a call that may overlap this one.  `out` may be q. */
