@@ -13,7 +13,7 @@
 // Work.  For one key head, the rows (token, query head of the group) of a
 // sequence are cut into tiles of kRows rows, and each tile has the key blocks
 // its rows can see.  All (part, sequence, key head, tile, key block) units lie
-// on one line, every tile preceded by kTileCost units for what a tile costs
+// on one line, every tile preceded by a few units for what a tile costs
 // besides its blocks; CTA c takes the c-th of equal intervals of it.  A CTA so gets
 // the end of one tile, whole tiles, and the start of another, whatever the
 // lengths are, and no length has to be known on the host.  A tile that lies in
@@ -76,12 +76,16 @@ struct PagedFrag {
   const int* page_list;
 };
 
-// Starting and ending a tile (query rows in, first scores, output) takes about
-// as long as two key blocks, measured on both kernels.
-constexpr int kTileCost = 2;
+// Starting and ending a tile (query rows in, first scores, output) in units of
+// a key block.  Measured on 8 canvases behind a 32768-token prefix (256-row
+// tiles): 2 units 285 us, 3 to 5 263 us; ragged causal prompts 129, 128.5,
+// 125 and 123 us for 2, 3, 4 and 5; on 64 single tokens (128-row tiles): 3
+// units 87.7 us, 4 90.0 us.
+constexpr int paged_tile_cost(int rows) { return rows == 256 ? 5 : rows == 128 ? 3 : 2; }
 
 template <int kRows, int kBlk>
 struct PagedWalk {
+  static constexpr int kTileCost = paged_tile_cost(kRows);
   const PagedAttnArgs& a;
   // (the host refuses batches whose line could reach 2^31 units)
   int x, x1;          // interval left: [x, x1)

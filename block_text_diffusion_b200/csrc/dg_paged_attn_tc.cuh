@@ -423,6 +423,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const int vis = min(sf.vis_max, sf.vis0 + sf.tok0 + tk);
       warp_arrive(&frag_empty[fi % kPaFrags]);
       if (nblk == 0) break;
+      const bool turns = !split;                      // (a split piece waits for memory, not for exponentials)
       const bool warp_on = wt * 32 < n_rows;         // rows past the piece's end do no work
       float m_run = -INFINITY, l_run = 0.0f;
       const int step = split ? 2 : 1, j0 = split ? t : 0;
@@ -471,8 +472,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           }
           // The exponential unit is what both softmaxes need most; the warps of A
           // and B on it take turns, so one exponentiates while the other's MMAs run.
-          // (A narrow piece waits for memory, not for exponentials.)
-          if (!kNarrow) {
+          if (turns) {
             ok = pa_wait(&turn[t][wt], turn_phase, err);
             turn_phase ^= 1;
             if (!ok) break;
@@ -498,12 +498,12 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
               warp_arrive(&p_part[t]);
             }
           }
-          if (!kNarrow && lane == 0) mbar_arrive(&turn[1 - t][wt]);
+          if (turns && lane == 0) mbar_arrive(&turn[1 - t][wt]);
           l_run = l_run * alpha + ((ls[0] + ls[1]) + (ls[2] + ls[3]));
           m_run = m_new;
           tmem_wait_st();
         } else {
-          if (!kNarrow) {
+          if (turns) {
             ok = pa_wait(&turn[t][wt], turn_phase, err);
             turn_phase ^= 1;
             if (!ok) break;
@@ -513,11 +513,6 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         tc_fence_before();
         warp_arrive(&p_full[t]);
-      }
-      if (!kNarrow && ok && split && t == 1 && (nblk & 1)) {     // A had one turn more
-        ok = pa_wait(&turn[1][wt], turn_phase, err);
-        turn_phase ^= 1;
-        if (ok) warp_arrive(&turn[0][wt]);
       }
       // ---------------- epilogue ----------------
       const bool both = split && nblk > 1;           // B has a half to join
