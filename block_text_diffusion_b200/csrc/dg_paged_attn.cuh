@@ -373,35 +373,46 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, 
   const long long rows = (long long)a.b.n_tokens * a.n_heads;
   const int parts = a.b.prefix_len > 0 ? 2 : 1;
   const int lo = a.b.n_seqs > 0 ? a.b.cu_q[0] : 0, hi = a.b.n_seqs > 0 ? a.b.cu_q[a.b.n_seqs] : 0;
-  for (long long row = ((long long)blockIdx.x * 16 + grp) / kShare; row < rows; row += (long long)gridDim.x * 16 / kShare) {
-    const int tok = (int)(row / a.n_heads), head = (int)(row % a.n_heads);
-    if (tok < lo || tok >= hi) continue;
-    int cta[2], r[2], n[2] = {0, 0};   // first CTA, row in the tile, pieces
-    bool final = false;
-    for (int p = 0; p < parts; ++p) {
-      const int2 m = a.meta[p * rows + row];
-      if (p == 0) final = m.x < 0;
-      // (what a row no tile covered finds here still stays in the workspace)
-      cta[p] = min(max(m.x, 0), grid_main - 1);
-      r[p] = m.y & (kRows - 1);
-      n[p] = 1 + min(max(m.y / kRows, 0), grid_main - 1 - cta[p]);
-    }
-    if (final) continue;   // written by the main kernel
+  const long long row_lo = (long long)lo * a.n_heads, row_hi = lmin((long long)hi * a.n_heads, rows);
+  // Without a prefix most rows are finished already.  Where a group has several
+  // rows its lanes look at their meta at once and it goes on to those that are
+  // not (chunks of as many rows as a group has, so none waits on another's).
+  const long long groups = (long long)gridDim.x * 16 / kShare;
+  const int chunk = kShare > 1 || parts == 2 ? 1 : (int)lmin(16, (rows + groups - 1) / groups);
+  for (long long c0 = ((long long)blockIdx.x * 16 + grp) / kShare * chunk; c0 < rows; c0 += groups * chunk) {
+   unsigned todo = 1;
+   if (chunk > 1) {
+     const long long mine = c0 + lane;
+     const bool open = lane < chunk && mine >= row_lo && mine < row_hi && a.meta[mine].x >= 0;
+     todo = __ballot_sync(0xffffu << (threadIdx.x & 16), open) >> (threadIdx.x & 16) & 0xffffu;
+   }
+   for (; todo; todo &= todo - 1) {
+    const long long row = c0 + __ffs(todo) - 1;
+    if (row < row_lo || row >= row_hi) continue;
+    const int tok = (int)((unsigned)row / (unsigned)a.n_heads), head = (int)row - tok * a.n_heads;
+    const int2 m0 = a.meta[row], m1 = parts == 2 ? a.meta[rows + row] : make_int2(0, 0);
+    if (m0.x < 0) continue;   // written by the main kernel
+    // first CTA, row in the tile, pieces of each part (what a row no tile
+    // covered finds here still stays in the workspace)
+    const int cta0 = min(max(m0.x, 0), grid_main - 1), cta1 = min(max(m1.x, 0), grid_main - 1);
+    const int r0 = m0.y & (kRows - 1), r1 = m1.y & (kRows - 1);
+    const int n0 = 1 + min(max(m0.y / kRows, 0), grid_main - 1 - cta0);
+    const int n = n0 + (parts == 2 ? 1 + min(max(m1.y / kRows, 0), grid_main - 1 - cta1) : 0);
     float acc[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
     float top = -INFINITY, sum = 0.0f;   // reference and sum of 2^(lse - top)
-    for (int i0 = share; i0 < n[0] + n[1]; i0 += kShare * kBatch) {
+    for (int i0 = share; i0 < n; i0 += kShare * kBatch) {
       float4 v[kBatch][kPer / 4];
       float lse[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         int i = i0 + u * kShare;
         lse[u] = -INFINITY;
-        if (i >= n[0] + n[1]) continue;
-        const int p = i >= n[0];
-        i -= p ? n[0] : 0;
-        const long long at = (long long)(cta[p] + i) * kRows + r[p];
+        if (i >= n) continue;
+        const int p = i >= n0;
+        i -= p ? n0 : 0;
+        const long long at = (long long)((p ? cta1 : cta0) + i) * kRows + (p ? r1 : r0);
         const float* o = i == 0 ? a.part_o + (p * rows + row) * kHd : a.slot_o + at * kHd;
         lse[u] = i == 0 ? a.part_lse[p * rows + row] : a.slot_lse[at];
 #pragma unroll
@@ -457,166 +468,264 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, 
         if (a.lse && threadIdx.x == 0) a.lse[row] = z > 0.0f ? (ref + log2f(z)) * kLn2 : -INFINITY;
       }
     }
+   }
   }
 }
 
 // ---------------------------------------------------------------------------
 // fp32: CUDA cores (the tensor cores have no fp32 product).  A CTA of 256
-// threads holds a tile of 64 rows and takes 64 keys at a time; thread (ty, tx)
-// owns the scores of rows 4 ty .. 4 ty + 3 and keys tx + 16 c, and of the
-// output the same rows with the columns 4 tx + 64 c ...
+// threads holds a tile of 64 rows and takes 64 keys at a time, the next block
+// on its way into the other half of a double buffer (asynchronous copies that
+// write zeros for keys past the last visible one, so what the cache holds
+// there never enters a sum).
+//
+// More than 8 rows: thread (ty, tx) owns the scores of rows 4 ty .. 4 ty + 3
+// and keys tx + 16 c, and of the output the same rows with columns 4 tx + 64 c;
+// warps whose rows lie past the piece's end only load.  Bound by the FMA pipe.
+// At most 8 rows (single tokens): that mapping would leave seven of eight
+// warps without a row, so a thread takes the scores of one key for two rows,
+// and warp r then has row r for the softmax and the product with V.  Bound by
+// memory.
 // ---------------------------------------------------------------------------
-constexpr int kPaF32Rows = 64, kPaF32Blk = 64;
+constexpr int kPaF32Rows = 64, kPaF32Blk = 64, kPaF32Few = 8;
 template <int kHd>
-constexpr int paged_f32_smem() {
-  // Q and K rows padded by 4 floats, V, P rows padded by 4
-  return (kPaF32Rows * (kHd + 4) + kPaF32Blk * (kHd + 4) + kPaF32Blk * kHd + kPaF32Rows * (kPaF32Blk + 4)) * 4;
+struct PaF32 {
+  static constexpr int kLd = kHd + 4;                                   // padded rows of Q and K
+  static constexpr int kKv = kPaF32Blk * (kLd + kHd);                   // floats of a block's K and V
+  static constexpr int kLdP = kPaF32Blk + 4;
+  static constexpr int kSmem = (kPaF32Rows * kLd + 2 * kKv + kPaF32Rows * kLdP) * 4;
+};
+
+// 16 bytes, zeros where not `ok`.
+__device__ __forceinline__ void cp_async_16z(float* dst, const float* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+
+// Where the output of a row of a piece goes, and its log-sum-exp (l2: base 2).
+__device__ __forceinline__ float* paged_f32_dest(const PagedAttnArgs& a, const PagedFrag& f, int r, int hd, float l2,
+                                                 bool writer) {
+  const int t = a.by_g.div(f.rem0 + r), tok = f.q0 + f.tok0 + t, head = f.kvh * a.G + f.rem0 + r - t * a.G;
+  const long long row = (long long)tok * a.n_heads + head;
+  const PagedDest d = paged_dest<kPaF32Rows>(a, f, r, hd, row);   // (every thread of the row stores the same meta)
+  if (writer) {
+    if (!d.final) *d.lse = l2;
+    else if (a.lse) a.lse[row] = l2 * kLn2;
+  }
+  return d.final ? (float*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs : d.o;
 }
 
 template <int kHd>
-__global__ void __launch_bounds__(256, 1) k_paged_attn_f32(PagedAttnArgs a) {
-  constexpr int R = kPaF32Rows, B = kPaF32Blk, kLd = kHd + 4, kLdP = B + 4, kOc = kHd / 64;
+__global__ void __launch_bounds__(256, 1) k_paged_attn_f32(const __grid_constant__ PagedAttnArgs a) {
+  using C = PaF32<kHd>;
+  constexpr int R = kPaF32Rows, B = kPaF32Blk, kLd = C::kLd, kLdP = C::kLdP, kOc = kHd / 64, kCh = kHd / 4;
   extern __shared__ __align__(16) float sm[];
   float* sQ = sm;
-  float* sK = sQ + R * kLd;
-  float* sV = sK + B * kLd;
-  float* sP = sV + B * kHd;
+  float* sKV = sQ + R * kLd;
+  float* sP = sKV + 2 * C::kKv;
   pdl_enter();
   PagedWalk<R, B> walk(a);
   if (!walk.begin()) return;   // (each warp finds the same)
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, warp = tid >> 5, lane = tid & 31;
+  const int page_mask = (1 << a.b.page_shift) - 1;
   for (;;) {
     const PagedFrag f = walk.next();
     if (f.nblk == 0) break;
-    __syncthreads();   // the previous piece is done with shared memory
-    for (int i = tid; i < R * (kHd / 4); i += 256) {
-      const int r = i / (kHd / 4), c = i % (kHd / 4) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < f.rows) {
-        const int t = a.by_g.div(f.rem0 + r);
-        v = *reinterpret_cast<const float4*>((const float*)a.q + (long long)(f.q0 + f.tok0 + t) * a.q_ts +
-                                             (long long)(f.kvh * a.G + f.rem0 + r - t * a.G) * a.q_hs + c);
+    auto issue = [&](int kb, int buf) {
+      float* sK = sKV + buf * C::kKv;
+      float* sV = sK + B * kLd;
+      for (int i = tid; i < B * kCh; i += 256) {
+        const int r = i / kCh, c = i % kCh * 4, key = kb * B + r;
+        bool ok = key < f.limit;
+        long long off = 0;
+        if (ok) {
+          const int page = f.page_list[key >> a.b.page_shift];
+          ok = page >= 0 && page < a.b.n_pages;
+          if (ok) off = ((((long long)page * a.n_kv_heads + f.kvh) << a.b.page_shift) + (key & page_mask)) * kHd + c;
+          else dev_error(a.b.status, kStatusState);
+        }
+        cp_async_16z(sK + r * kLd + c, (const float*)a.k_pages + off, ok);
+        cp_async_16z(sV + r * kHd + c, (const float*)a.v_pages + off, ok);
       }
-      *reinterpret_cast<float4*>(sQ + r * kLd + c) = v;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncthreads();   // the previous piece is done with shared memory
+    for (int i = tid; i < R * kCh; i += 256) {
+      const int r = i / kCh, c = i % kCh * 4;
+      const bool ok = r < f.rows;
+      const int t = ok ? a.by_g.div(f.rem0 + r) : 0;
+      const float* src = (const float*)a.q;
+      if (ok)
+        src += (long long)(f.q0 + f.tok0 + t) * a.q_ts + (long long)(f.kvh * a.G + f.rem0 + r - t * a.G) * a.q_hs + c;
+      cp_async_16z(sQ + r * kLd + c, src, ok);
     }
+    issue(f.kb0, 0);
+    const bool few = f.rows <= kPaF32Few;
+    const bool on = few ? warp < f.rows : warp * 8 < f.rows;
     int vis[4];
     float top[4], sum[4], o[4][4 * kOc];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      vis[i] = min(f.vis_max, f.vis0 + f.tok0 + a.by_g.div(f.rem0 + ty * 4 + i));
+      vis[i] = min(f.vis_max, f.vis0 + f.tok0 + a.by_g.div(f.rem0 + (few ? warp : ty * 4 + i)));
       top[i] = -INFINITY;
       sum[i] = 0.0f;
 #pragma unroll
       for (int c = 0; c < 4 * kOc; ++c) o[i][c] = 0.0f;
     }
-    for (int kb = f.kb0; kb < f.kb0 + f.nblk; ++kb) {
-      const int key0 = kb * B;
-      __syncthreads();
-      // keys and values of the block; rows past the last visible key are zero,
-      // so what the cache holds there never enters a sum
-      for (int i = tid; i < B * (kHd / 4); i += 256) {
-        const int r = i / (kHd / 4), c = i % (kHd / 4) * 4, key = key0 + r;
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        if (key < f.limit) {
-          const int page = f.page_list[key >> a.b.page_shift];
-          if (page >= 0 && page < a.b.n_pages) {
-            const long long off = ((((long long)page * a.n_kv_heads + f.kvh) << a.b.page_shift) +
-                                   (key & ((1 << a.b.page_shift) - 1))) * kHd + c;
-            k = *reinterpret_cast<const float4*>((const float*)a.k_pages + off);
-            v = *reinterpret_cast<const float4*>((const float*)a.v_pages + off);
-          } else {
-            dev_error(a.b.status, kStatusState);
-          }
-        }
-        *reinterpret_cast<float4*>(sK + r * kLd + c) = k;
-        *reinterpret_cast<float4*>(sV + r * kHd + c) = v;
+    for (int j = 0; j < f.nblk; ++j) {
+      const int key0 = (f.kb0 + j) * B;
+      const float* sK = sKV + (j & 1) * C::kKv;
+      const float* sV = sK + B * kLd;
+      if (j + 1 < f.nblk) {
+        issue(f.kb0 + j + 1, (j + 1) & 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       __syncthreads();
-      float s[4][4];
+      if (few) {
+        // scores of key tid % 64 for rows 2 (tid / 64) and the next
+        const int key = tid & 63, r0 = tid >> 6 << 1;
+        if (r0 < f.rows) {
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 8
+          for (int d = 0; d < kHd; d += 4) {
+            const float4 k = *reinterpret_cast<const float4*>(sK + key * kLd + d);
+            const float4 q0 = *reinterpret_cast<const float4*>(sQ + r0 * kLd + d);
+            const float4 q1 = *reinterpret_cast<const float4*>(sQ + (r0 + 1) * kLd + d);
+            s0 += q0.x * k.x + q0.y * k.y + q0.z * k.z + q0.w * k.w;
+            s1 += q1.x * k.x + q1.y * k.y + q1.z * k.z + q1.w * k.w;
+          }
+          sP[r0 * kLdP + key] = s0 * a.scale_log2;
+          sP[(r0 + 1) * kLdP + key] = s1 * a.scale_log2;
+        }
+        __syncthreads();
+        if (on) {
+          float x[2], mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+          for (int u = 0; u < 2; ++u) {
+            x[u] = key0 + lane + 32 * u < vis[0] ? sP[warp * kLdP + lane + 32 * u] : -INFINITY;
+            mx = fmaxf(mx, x[u]);
+          }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+          for (int w = 16; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          const float up = fmaxf(top[0], mx), old = top[0] == -INFINITY ? 0.0f : exp2f(top[0] - up);
+          float add = 0.0f;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float p = up == -INFINITY ? 0.0f : exp2f(x[u] - up);
+            add += p;
+            sP[warp * kLdP + lane + 32 * u] = p;
+          }
+          sum[0] = sum[0] * old + warp_sum(add);
+          top[0] = up;
+          __syncwarp();
+          // columns 2 lane + 64 c and the next
+#pragma unroll
+          for (int c = 0; c < 2 * kOc; ++c) o[0][c] *= old;
 #pragma unroll 4
-      for (int d = 0; d < kHd; d += 4) {
-        float4 qv[4], kv[4];
+          for (int k = 0; k < B; k += 4) {
+            const float4 p = *reinterpret_cast<const float4*>(sP + warp * kLdP + k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty * 4 + i) * kLd + d);
+            for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * kLd + d);
+              for (int c = 0; c < kOc; ++c) {
+                const float2 v = *reinterpret_cast<const float2*>(sV + (k + kk) * kHd + c * 64 + lane * 2);
+                const float pp = kk == 0 ? p.x : kk == 1 ? p.y : kk == 2 ? p.z : p.w;
+                o[0][2 * c] += pp * v.x;
+                o[0][2 * c + 1] += pp * v.y;
+              }
+          }
+        }
+      } else if (on) {
+        float s[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            s[i][j] += qv[i].x * kv[j].x + qv[i].y * kv[j].y + qv[i].z * kv[j].z + qv[i].w * kv[j].w;
-      }
+          for (int k = 0; k < 4; ++k) s[i][k] = 0.0f;
+#pragma unroll 4
+        for (int d = 0; d < kHd; d += 4) {
+          float4 qv[4], kv[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float mx = -INFINITY;
+          for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty * 4 + i) * kLd + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = key0 + tx + 16 * j < vis[i] ? s[i][j] * a.scale_log2 : -INFINITY;
-          mx = fmaxf(mx, s[i][j]);
+          for (int k = 0; k < 4; ++k) kv[k] = *reinterpret_cast<const float4*>(sK + (tx + 16 * k) * kLd + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              s[i][k] += qv[i].x * kv[k].x + qv[i].y * kv[k].y + qv[i].z * kv[k].z + qv[i].w * kv[k].w;
         }
 #pragma unroll
-        for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float up = fmaxf(top[i], mx);
-        const float old = top[i] == -INFINITY ? 0.0f : exp2f(top[i] - up);
-        float add = 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p = up == -INFINITY ? 0.0f : exp2f(s[i][j] - up);
-          add += p;
-          sP[(ty * 4 + i) * kLdP + tx + 16 * j] = p;
-        }
-#pragma unroll
-        for (int w = 8; w; w >>= 1) add += __shfl_xor_sync(0xffffffffu, add, w);
-        sum[i] = sum[i] * old + add;
-        top[i] = up;
-#pragma unroll
-        for (int c = 0; c < 4 * kOc; ++c) o[i][c] *= old;
-      }
-      __syncwarp();   // rows 4 ty .. belong to one half warp
-#pragma unroll 2
-      for (int k = 0; k < B; k += 4) {
-        float4 p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * 4 + i) * kLdP + k);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int c = 0; c < kOc; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(sV + (k + kk) * kHd + c * 64 + tx * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float pp = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-              o[i][c * 4] += pp * v.x;
-              o[i][c * 4 + 1] += pp * v.y;
-              o[i][c * 4 + 2] += pp * v.z;
-              o[i][c * 4 + 3] += pp * v.w;
-            }
+          for (int k = 0; k < 4; ++k) {
+            s[i][k] = key0 + tx + 16 * k < vis[i] ? s[i][k] * a.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, s[i][k]);
           }
+#pragma unroll
+          for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          const float up = fmaxf(top[i], mx);
+          const float old = top[i] == -INFINITY ? 0.0f : exp2f(top[i] - up);
+          float add = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float p = up == -INFINITY ? 0.0f : exp2f(s[i][k] - up);
+            add += p;
+            sP[(ty * 4 + i) * kLdP + tx + 16 * k] = p;
+          }
+#pragma unroll
+          for (int w = 8; w; w >>= 1) add += __shfl_xor_sync(0xffffffffu, add, w);
+          sum[i] = sum[i] * old + add;
+          top[i] = up;
+#pragma unroll
+          for (int c = 0; c < 4 * kOc; ++c) o[i][c] *= old;
+        }
+        __syncwarp();   // rows 4 ty .. belong to one half warp
+#pragma unroll 2
+        for (int k = 0; k < B; k += 4) {
+          float4 p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * 4 + i) * kLdP + k);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int c = 0; c < kOc; ++c) {
+              const float4 v = *reinterpret_cast<const float4*>(sV + (k + kk) * kHd + c * 64 + tx * 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float pp = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                o[i][c * 4] += pp * v.x;
+                o[i][c * 4 + 1] += pp * v.y;
+                o[i][c * 4 + 2] += pp * v.z;
+                o[i][c * 4 + 3] += pp * v.w;
+              }
+            }
+        }
       }
+      __syncthreads();   // the block's buffer is free
+    }
+    if (few) {
+      if (on) {
+        const float inv = sum[0] > 0.0f ? 1.0f / sum[0] : 0.0f;
+        float* dst = paged_f32_dest(a, f, warp, kHd, sum[0] > 0.0f ? top[0] + log2f(sum[0]) : -INFINITY, lane == 0);
+#pragma unroll
+        for (int c = 0; c < kOc; ++c)
+          *reinterpret_cast<float2*>(dst + c * 64 + lane * 2) = make_float2(o[0][2 * c] * inv, o[0][2 * c + 1] * inv);
+      }
+      continue;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= f.rows) continue;
-      const int t = a.by_g.div(f.rem0 + r), tok = f.q0 + f.tok0 + t, head = f.kvh * a.G + f.rem0 + r - t * a.G;
-      const long long row = (long long)tok * a.n_heads + head;
       const float inv = sum[i] > 0.0f ? 1.0f / sum[i] : 0.0f;
-      const float l2 = sum[i] > 0.0f ? top[i] + log2f(sum[i]) : -INFINITY;
-      // (all 16 threads of the row store the same meta)
-      const PagedDest d = paged_dest<R>(a, f, r, kHd, row);
-      float* dst = d.final ? (float*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs : d.o;
+      float* dst = paged_f32_dest(a, f, r, kHd, sum[i] > 0.0f ? top[i] + log2f(sum[i]) : -INFINITY, tx == 0);
 #pragma unroll
       for (int c = 0; c < kOc; ++c)
         *reinterpret_cast<float4*>(dst + c * 64 + tx * 4) =
             make_float4(o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv);
-      if (tx == 0) {
-        if (!d.final) *d.lse = l2;
-        else if (a.lse) a.lse[row] = l2 * kLn2;
-      }
     }
   }
 }

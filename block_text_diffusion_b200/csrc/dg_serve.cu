@@ -247,8 +247,8 @@ dg_status run_paged_attention(const dg_paged_kv* c, PagedAttnArgs& a, cudaStream
     e = narrow ? launch_tc<kHd, true>(tk, tv, a, s) : launch_tc<kHd, false>(tk, tv, a, s);
   } else {
     static std::atomic<uint64_t> raised{0};
-    e = raise_smem(k_paged_attn_f32<kHd>, paged_f32_smem<kHd>(), raised);
-    if (e == cudaSuccess) e = launch(k_paged_attn_f32<kHd>, kSMs, 256, paged_f32_smem<kHd>(), s, a);
+    e = raise_smem(k_paged_attn_f32<kHd>, PaF32<kHd>::kSmem, raised);
+    if (e == cudaSuccess) e = launch(k_paged_attn_f32<kHd>, kSMs, 256, PaF32<kHd>::kSmem, s, a);
   }
   if (e != cudaSuccess) return done(e);
   return c->dtype == DG_BF16 ? run_join<bf16, kHd>(a, narrow ? 128 : 256, s) : run_join<float, kHd>(a, kPaF32Rows, s);
