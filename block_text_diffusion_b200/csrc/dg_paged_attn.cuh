@@ -119,27 +119,26 @@ struct PagedWalk {
     p.kv = b.prefix_len;
     return p;
   }
-  // units of the tiles of one sequence for one key head (a whole warp asks for one sequence)
-  DG_HD long long units_of(const PagedSeq& q, int part_) const {
+  // Units of the tiles of one sequence for one key head (a whole warp asks for
+  // one sequence).  Unsigned and without a check: a batch that passes the
+  // host's bound fits, and offsets that overlap (reported by paged_seq) only
+  // leave rows uncovered, whatever the sums wrap to.
+  DG_HD unsigned units_of(const PagedSeq& q, int part_) const {
     const int n = tiles_of(q);
-    if (part_ == 1 || !a.causal || n < 2) return n == 0 ? 0 : (long long)n * tile_units(q, part_, 0);
-    long long sum = 0;
+    if (part_ == 1 || !a.causal || n < 2) return n == 0 ? 0 : (unsigned)n * tile_units(q, part_, 0);
+    unsigned sum = 0;
 #ifdef __CUDA_ARCH__
     for (int i = threadIdx.x & 31; i < n; i += 32) sum += tile_units(q, 0, i);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sum = __reduce_add_sync(0xffffffffu, sum);
 #else
     for (int i = 0; i < n; ++i) sum += tile_units(q, 0, i);
 #endif
     return sum;
   }
-  // Interval `cta` of `grid` equal ones of a line of `total` units; false if it is empty.
-  DG_HD bool take_interval(long long total, int cta, int grid) {
-    if (total >> 31) {   // (offsets that overlap)
-      paged_error(a.b, kStatusState);
-      return false;
-    }
-    per = imax(1, (int)(((unsigned)total + grid - 1u) / (unsigned)grid));
+  // Interval `cta` of kSMs equal ones of a line of `total` units; false if it is empty.
+  DG_HD bool take_interval(unsigned total, int cta) {
+    total &= 0x7fffffffu;
+    per = imax(1, (int)((total + kSMs - 1u) / kSMs));
     x = (int)lmin(total, (long long)cta * per);
     x1 = (int)lmin(total, (long long)x + per);
     return x < x1;
@@ -154,16 +153,17 @@ struct PagedWalk {
     tile = (x - kvh * each) / len;
     tile_x0 = kvh * each + tile * len;
   }
-  // x lies in sequence i, which starts at x0 on the line (a whole warp)
-  DG_HD void enter_sequence(int i, int x0) {
+  // x lies in sequence i = q, which starts at x0 on the line (a whole warp)
+  DG_HD void enter_sequence(int i, const PagedSeq& q, int x0) {
     part = 0;
     seq = i;
-    s = paged_seq(a.b, i);
+    s = q;
     n_tiles = tiles_of(s);
     tile = 0;
-    const int each = imax(1, (int)units_of(s, 0));
-    kvh = imin(a.n_kv_heads - 1, (x - x0) / each);
-    tile_x0 = x0 + kvh * each;
+    const unsigned each = units_of(s, 0);
+    kvh = each ? imin(a.n_kv_heads - 1, (int)((unsigned)(x - x0) / each)) : 0;
+    tile_x0 = x0 + kvh * (int)each;
+    if (n_tiles < 2) return;
     if (!a.causal) {   // tiles of one length
       const int len = tile_units(s, 0, 0);
       tile = imin(n_tiles - 1, (x - tile_x0) / len);
@@ -196,45 +196,44 @@ struct PagedWalk {
   }
 
 #ifdef __CUDACC__
-  // Units of sequence base + lane, for all key heads (0 past the last).
-  __device__ __noinline__ long long lane_units(int base) const {
+  // Sequence base + lane and its units for all key heads (0 past the last).
+  __device__ __noinline__ unsigned lane_units(int base, PagedSeq& q) const {
     const int lane = threadIdx.x & 31;
-    PagedSeq q{0, 0, 0};
+    q = PagedSeq{0, 0, 0};
     if (base + lane < a.b.n_seqs) q = paged_seq(a.b, base + lane);
     // one tile, or tiles of one length: by the lane; the others by the warp
     const int n = tiles_of(q);
     const bool many = a.causal && n > 1;
-    long long u = n == 0 || many ? 0 : (long long)n * tile_units(q, 0, 0);
+    unsigned u = n == 0 || many ? 0 : (unsigned)n * tile_units(q, 0, 0);
     for (unsigned m = __ballot_sync(0xffffffffu, many); m; m &= m - 1) {
       const int l = __ffs(m) - 1;
-      const long long v = units_of(PagedSeq{0, __shfl_sync(0xffffffffu, q.nq, l), __shfl_sync(0xffffffffu, q.kv, l)}, 0);
+      const unsigned v = units_of(PagedSeq{0, __shfl_sync(0xffffffffu, q.nq, l), __shfl_sync(0xffffffffu, q.kv, l)}, 0);
       if (lane == l) u = v;
     }
     return u * a.n_kv_heads;
   }
 
   // Finds the CTA's interval and where it starts, by one warp; false if there
-  // is nothing to do.
+  // is nothing to do.  Up to 32 sequences are read once.
   __device__ bool begin() {
     const int lane = threadIdx.x & 31, n = a.b.n_seqs;
-    long long mine = 0;
-#pragma unroll 1
-    for (int base = 0; base < n; base += 32) mine += lane_units(base);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    long long each = 0;
+    PagedSeq q;
+    unsigned u = lane_units(0, q), mine = u;
+    unsigned each = 0;
     if (a.b.prefix_len > 0) each = units_of(whole_batch(), 1);
-    const long long pre = each * a.n_kv_heads;
-    if (!take_interval(mine + pre, blockIdx.x, gridDim.x)) return false;
-    if (x < pre) {
+#pragma unroll 1
+    for (int base = 32; base < n; base += 32) mine += lane_units(base, q);
+    const unsigned pre = each * a.n_kv_heads;
+    if (!take_interval(__reduce_add_sync(0xffffffffu, mine) + pre, blockIdx.x)) return false;
+    if ((unsigned)x < pre) {
       enter_prefix((int)each);
       return true;
     }
     int at = (int)pre;
 #pragma unroll 1
     for (int base = 0; base < n; base += 32) {
-      const int len = (int)lane_units(base);
-      int incl = len;
+      if (n > 32) u = lane_units(base, q);
+      int incl = (int)u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -243,7 +242,9 @@ struct PagedWalk {
       const unsigned past = __ballot_sync(0xffffffffu, x < at + incl);
       if (past) {
         const int k = __ffs(past) - 1;
-        enter_sequence(base + k, at + __shfl_sync(0xffffffffu, incl - len, k));
+        const PagedSeq f{__shfl_sync(0xffffffffu, q.q0, k), __shfl_sync(0xffffffffu, q.nq, k),
+                         __shfl_sync(0xffffffffu, q.kv, k)};
+        enter_sequence(base + k, f, at + __shfl_sync(0xffffffffu, incl - (int)u, k));
         return true;
       }
       at += __shfl_sync(0xffffffffu, incl, 31);
@@ -253,21 +254,22 @@ struct PagedWalk {
 #endif
 
   // The same on the host, for a batch in host memory.
-  bool begin_host(int cta, int grid) {
-    const long long each = a.b.prefix_len > 0 && a.b.n_seqs > 0 ? units_of(whole_batch(), 1) : 0;
-    const long long pre = each * a.n_kv_heads;
-    long long total = pre;
+  bool begin_host(int cta) {
+    const unsigned each = a.b.prefix_len > 0 && a.b.n_seqs > 0 ? units_of(whole_batch(), 1) : 0;
+    const unsigned pre = each * a.n_kv_heads;
+    unsigned total = pre;
     for (int i = 0; i < a.b.n_seqs; ++i) total += units_of(paged_seq(a.b, i), 0) * a.n_kv_heads;
-    if (!take_interval(total, cta, grid)) return false;
-    if (x < pre) {
+    if (!take_interval(total, cta)) return false;
+    if ((unsigned)x < pre) {
       enter_prefix((int)each);
       return true;
     }
     int at = (int)pre;
     for (int i = 0; i < a.b.n_seqs; ++i) {
-      const int n = (int)units_of(paged_seq(a.b, i), 0) * a.n_kv_heads;
+      const PagedSeq q = paged_seq(a.b, i);
+      const int n = (int)(units_of(q, 0) * a.n_kv_heads);
       if (x < at + n) {
-        enter_sequence(i, at);
+        enter_sequence(i, q, at);
         return true;
       }
       at += n;

@@ -136,6 +136,21 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// The last block of a piece.  Its keys past the last visible one are masked in
+// S, so P is 0 there, but 0 times whatever their values hold (the cache may
+// hold anything) is not 0 for an infinity or a NaN: the product with V stops
+// after the last 16 keys that hold a visible one, and the rows of V past it in
+// those 16 become zeros.
+struct PaTail {
+  int valid, steps;   // visible keys of the block, MMAs of 16 keys (one at least)
+  bool clear;
+  __device__ __forceinline__ PaTail(const PagedFrag& f) {
+    valid = max(0, min(kPaBlk, f.limit - (f.kb0 + f.nblk - 1) * kPaBlk));
+    steps = max(1, (valid + 15) >> 4);
+    clear = steps * 16 != valid;
+  }
+};
+
 template <int kHd, bool kNarrow>
 __global__ void __launch_bounds__(kPaThreads, 1)
 k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -262,7 +277,8 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!ok) break;
         const PagedFrag& sf = s_frag[fi % kPaFrags];
         const int n = sf.nblk;
-        const bool wide = !kNarrow && sf.rows > 128, tail = sf.limit < (sf.kb0 + n) * kPaBlk;
+        const bool wide = !kNarrow && sf.rows > 128;
+        const PaTail tail(sf);
         mbar_arrive(&frag_empty[fi % kPaFrags]);
         if (n == 0) break;
         // (both threads follow every phase of q_full[0], needed or not: a parity
@@ -295,7 +311,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           if (do_v) v_slot = take(wide ? 2 * j + 1 : j == n - 1 ? 2 * n - 1 : 2 * j + 2);
           if (do_k && ok) k_slot = take(wide ? 2 * jn : jn == 0 ? 0 : 2 * jn - 1);
           if (do_v && ok) {
-            if (tail && j == n - 1) {
+            if (tail.clear && j == n - 1) {
               // warp 10 clears the rows past the last key once every user of the
               // block is here (the softmax still runs)
               mbar_arrive(&v_last);
@@ -311,19 +327,20 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             // under the exponentials of the rest
             const uint64_t vd = v_base + v_slot * (C::kBytes >> 4);
             const uint32_t acc = j > j_first ? 1u : 0u;
+            const int steps = j == n - 1 ? tail.steps : kPaBlk / 16;
             ok = pa_wait_one(&p_part[t], p_phase, err);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kPaPart / 16; ++kk)
-              tc_mma_bf16_ta(dO, dS + kk * 8, vd + kk * (2048 >> 4), kIdO, kk > 0 ? 1u : acc);
+              if (kk < steps) tc_mma_bf16_ta(dO, dS + kk * 8, vd + kk * (2048 >> 4), kIdO, kk > 0 ? 1u : acc);
             ok = pa_wait_one(&p_full[t], p_phase, err);
             p_phase ^= 1;
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = kPaPart / 16; kk < kPaBlk / 16; ++kk)
-              tc_mma_bf16_ta(dO, dS + kk * 8, vd + kk * (2048 >> 4), kIdO, 1u);
+              if (kk < steps) tc_mma_bf16_ta(dO, dS + kk * 8, vd + kk * (2048 >> 4), kIdO, 1u);
           }
           if (do_k) {
             const uint64_t kd = k_base + k_slot * (C::kBytes >> 4);
@@ -357,7 +374,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       if (!ok) break;
       const PagedFrag& sf = s_frag[fi % kPaFrags];
       const int n = sf.nblk, rows = sf.rows, rem0 = sf.rem0;
-      const int valid = max(0, sf.limit - (sf.kb0 + n - 1) * kPaBlk);   // visible keys of the last block
+      const PaTail tail(sf);
       const bf16* src = (const bf16*)a.q + (long long)(sf.q0 + sf.tok0) * a.q_ts +
                         (long long)(sf.kvh * a.G + rem0) * a.q_hs + c * 8;
       warp_arrive(&frag_empty[fi % kPaFrags]);
@@ -380,18 +397,16 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         fence_async_smem();
         warp_arrive(&q_full[t]);
       }
-      if (ok && valid < kPaBlk) {
-        // Keys past the last visible one are masked in S, but 0 times whatever
-        // their values hold (the cache may hold anything there) is not 0 for an
-        // infinity or a NaN: their rows of V, the piece's last block, become zeros.
+      if (ok && tail.clear) {
         const int s = (blocks - 1) % ST;
         ok = pa_wait(&v_last, tails++ & 1, err);
         if (!ok) break;
+        const int n16 = (tail.steps * 16 - tail.valid) * 8;
+#pragma unroll
+        for (int g = 0; g < C::kHalves; ++g)
 #pragma unroll 1
-        for (int i = lane; i < (kPaBlk - valid) * 8 * C::kHalves; i += 32) {
-          const int g = i / ((kPaBlk - valid) * 8), at = i - g * ((kPaBlk - valid) * 8);
-          *reinterpret_cast<uint4*>(sKV + s * C::kBytes + g * 16384 + valid * 128 + at * 16) = make_uint4(0, 0, 0, 0);
-        }
+          for (int i = lane; i < n16; i += 32)
+            *reinterpret_cast<uint4*>(sKV + s * C::kBytes + g * 16384 + tail.valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
         fence_async_smem();
         __syncwarp();
         const bool wide = !kNarrow && rows > 128;

@@ -375,7 +375,7 @@ extern "C" dg_status dg_test_paged_walk(const dg_paged_kv* cache, const dg_paged
   int n = 0;
   auto walk = [&](auto w) {
     for (int cta = 0; cta < kSMs; ++cta) {
-      if (!w.begin_host(cta, kSMs)) continue;
+      if (!w.begin_host(cta)) continue;
       for (PagedFrag f = w.next(); f.nblk; f = w.next(), ++n) {
         if (n >= cap) return false;
         const int seq = f.part ? -1 : (int)((f.page_list - a.b.table) / std::max<int64_t>(1, a.b.table_stride));
