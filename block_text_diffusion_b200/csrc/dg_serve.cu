@@ -84,10 +84,12 @@ dg_status done(cudaError_t e) {
 int elem_size(int dtype) { return dtype == DG_BF16 ? 2 : 4; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-// Largest |offset| a row of heads reaches stays far inside 64 bits.
-bool heads_ok(const dg_heads* h) {
+// Largest |offset| a row of heads reaches stays far inside 64 bits.  Buffers of
+// no rows may have no address.
+bool heads_ok(const dg_heads* h, int64_t n_tokens) {
   const int64_t lim = (int64_t)1 << 40;
-  return h && h->data && h->token_stride >= 0 && h->head_stride >= 0 && h->token_stride < lim && h->head_stride < lim;
+  return h && (h->data || n_tokens == 0) && h->token_stride >= 0 && h->head_stride >= 0 && h->token_stride < lim &&
+         h->head_stride < lim;
 }
 
 bool rope_ok(const dg_rope* r, int head_dim) {
@@ -262,11 +264,11 @@ extern "C" dg_status dg_qk_norm_rope(int32_t dtype, int32_t n_tokens, int32_t n_
                                      const dg_head_norm* norm, void* stream) {
   if ((dtype != DG_FP32 && dtype != DG_BF16) || n_tokens < 0 || n_heads < 0 || n_kv_heads < 0) return DG_ERR_INVALID_ARG;
   if (head_dim < 2 || head_dim > 256 || head_dim % 2) return DG_ERR_INVALID_ARG;
-  if (n_heads > 0 && (!heads_ok(q) || !heads_ok(q_out))) return DG_ERR_INVALID_ARG;
-  if (n_kv_heads > 0 && (!heads_ok(k) || !heads_ok(k_out))) return DG_ERR_INVALID_ARG;
+  if (n_heads > 0 && (!heads_ok(q, n_tokens) || !heads_ok(q_out, n_tokens))) return DG_ERR_INVALID_ARG;
+  if (n_kv_heads > 0 && (!heads_ok(k, n_tokens) || !heads_ok(k_out, n_tokens))) return DG_ERR_INVALID_ARG;
   if ((int64_t)n_heads + n_kv_heads > 65536) return DG_ERR_INVALID_ARG;
   if (!rope_ok(rope, head_dim) || !norm_ok(norm)) return DG_ERR_INVALID_ARG;
-  if (rope && rope->rot_dim > 0 && !positions) return DG_ERR_INVALID_ARG;
+  if (rope && rope->rot_dim > 0 && !positions && n_tokens > 0) return DG_ERR_INVALID_ARG;
   HeadRowsArgs a{};
   a.n_tokens = n_tokens;
   a.n_q = n_heads;
@@ -283,8 +285,10 @@ extern "C" dg_status dg_paged_append(const dg_paged_kv* cache, const dg_paged_ba
                                      const dg_heads* v, const dg_rope* rope, const dg_head_norm* norm,
                                      int32_t n_heads, const dg_heads* q, const dg_heads* q_out,
                                      int32_t* status_word, void* stream) {
-  if (!cache_ok(cache) || !batch_ok(cache, batch) || !heads_ok(k) || !heads_ok(v)) return DG_ERR_INVALID_ARG;
-  if (n_heads < 0 || (n_heads > 0 && (!heads_ok(q) || !heads_ok(q_out)))) return DG_ERR_INVALID_ARG;
+  if (!cache_ok(cache) || !batch_ok(cache, batch)) return DG_ERR_INVALID_ARG;
+  const int64_t rows = batch->n_tokens;
+  if (!heads_ok(k, rows) || !heads_ok(v, rows)) return DG_ERR_INVALID_ARG;
+  if (n_heads < 0 || (n_heads > 0 && (!heads_ok(q, rows) || !heads_ok(q_out, rows)))) return DG_ERR_INVALID_ARG;
   if ((int64_t)n_heads + 2ll * cache->n_kv_heads > 65536) return DG_ERR_INVALID_ARG;
   if (!rope_ok(rope, cache->head_dim) || !norm_ok(norm)) return DG_ERR_INVALID_ARG;
   HeadRowsArgs a{};
@@ -323,7 +327,7 @@ extern "C" dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return DG_OK;
   const int per16 = 16 / elem_size(cache->dtype);
   for (const dg_heads* h : {q, out})
-    if (!heads_ok(h) || !aligned(h->data, 16) || h->token_stride % per16 || h->head_stride % per16)
+    if (!heads_ok(h, batch->n_tokens) || !aligned(h->data, 16) || h->token_stride % per16 || h->head_stride % per16)
       return DG_ERR_INVALID_ARG;
   // The line of work units (see dg_paged_attn.cuh) is counted in 32 bits: at
   // most this many tiles of 64 rows, each with every block of 64 keys.

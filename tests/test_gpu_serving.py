@@ -213,6 +213,7 @@ APPEND = [
     (F32, 4, 4, 64, 16, 64, False, [17, 1, 64], [0, 16, 3], 33),
     (F32, 2, 1, 128, 128, 128, True, [129], [127], 0),
     (F32, 0, 3, 64, 32, 0, False, [1] * 70, list(range(70)), 0),
+    (BF, 2, 1, 64, 16, 64, False, [1, 0, 2] * 700, [3, 1, 14] * 700, 9),
 ]
 
 
@@ -334,6 +335,9 @@ ATTN = [
     (2, 1, 64, 16, False, [3, 5, 2], [-3, 20, -2], 0),   # sequences without a key
     (8, 8, 128, 64, True, [1] * 200, [i * 7 % 180 for i in range(200)], 0),
     (8, 2, 128, 32, True, [30] * 60, [300] * 60, 0),     # several joined halves of 120 rows in one CTA
+    (130, 1, 64, 16, True, [3, 1], [9, 200], 20),        # more query heads than a half tile has rows
+    (2, 2, 64, 16, True, [1, 0, 3] * 500, [5, 9, 0] * 500, 3),   # more sequences than a warp looks at at once
+    (4, 2, 128, 64, True, [90] * 40 + [400], [7] * 41, 0),       # many tiles in more than 32 sequences
 ]
 
 
@@ -535,6 +539,27 @@ def test_binding_refuses_mismatched_tensors():
     with pytest.raises(dg.DGError):   # rows off the 16-byte grid
         x = randn(gen(3), 2, 4, 66, dtype=BF)[..., :64]
         dg.paged_attention(b.cache, b.batch, x, q)
+
+
+def test_calls_without_rows_do_nothing():
+    b = Batch(71, BF, 2, 64, 16, [1], [5])
+    q, k = torch.empty(0, 4, 64, dtype=BF, device="cuda"), torch.empty(0, 2, 64, dtype=BF, device="cuda")
+    none = dg.PagedBatch(i32([0]), i32([]), torch.empty(0, 1, dtype=torch.int32, device="cuda"))
+    empty = dg.PagedBatch(i32([0, 0]), i32([6]), i32(b.table))
+    k0 = b.k.clone()
+    for batch in (none, empty):
+        dg.paged_append(b.cache, batch, k, k, q=q, q_out=q)
+        dg.paged_attention(b.cache, batch, q, q)
+    w, _ = freqs(64)
+    dg.qk_norm_rope(q, k, i32([]), q, k, rope=dg.Rope(w))
+    # rows, but no sequence to own them
+    x = torch.full((3, 4, 64), 2.0, dtype=BF, device="cuda")
+    y = torch.full((3, 2, 64), 2.0, dtype=BF, device="cuda")
+    out = torch.full_like(x, 5.0)
+    for batch in (none, empty):
+        dg.paged_append(b.cache, batch, y, y, q=x, q_out=out)
+        dg.paged_attention(b.cache, batch, x, out)
+    assert torch.all(out == 5.0) and torch.equal(b.k, k0)
 
 
 # -- together ----------------------------------------------------------------------
