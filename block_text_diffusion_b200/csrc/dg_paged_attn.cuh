@@ -438,12 +438,12 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, 
     }
     T* dst = (T*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs;
     if (kShare == 1) {
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
       for (int c = 0; c < kPer / 4; ++c)
         store4<T>(dst + c * 64 + lane * 4, acc[c * 4] * inv, acc[c * 4 + 1] * inv, acc[c * 4 + 2] * inv,
                   acc[c * 4 + 3] * inv);
-      if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+      if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     } else {
       // (the whole block is on one row: the branches above were uniform)
       __syncthreads();
@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, 
           x += s_acc[g % (kShare > 1 ? 16 : 1)][threadIdx.x] * w;
           z += s_sum[g] * w;
         }
-        dst[threadIdx.x] = from_f<T>(z > 0.0f ? x / z : 0.0f);
-        if (a.lse && threadIdx.x == 0) a.lse[row] = z > 0.0f ? (ref + log2f(z)) * kLn2 : -INFINITY;
+        dst[threadIdx.x] = from_f<T>(z == 0.0f ? 0.0f : x / z);
+        if (a.lse && threadIdx.x == 0) a.lse[row] = z == 0.0f ? -INFINITY : (ref + log2f(z)) * kLn2;
       }
     }
    }
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(const __grid_constant
           float add = 0.0f;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float p = up == -INFINITY ? 0.0f : exp2f(x[u] - up);
+            const float p = x[u] == -INFINITY ? 0.0f : exp2f(x[u] - up);
             add += p;
             sP[warp * kLdP + lane + 32 * u] = p;
           }
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(const __grid_constant
           float add = 0.0f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float p = up == -INFINITY ? 0.0f : exp2f(s[i][k] - up);
+            const float p = s[i][k] == -INFINITY ? 0.0f : exp2f(s[i][k] - up);
             add += p;
             sP[(ty * 4 + i) * kLdP + tx + 16 * k] = p;
           }
@@ -710,8 +710,8 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(const __grid_constant
     }
     if (few) {
       if (on) {
-        const float inv = sum[0] > 0.0f ? 1.0f / sum[0] : 0.0f;
-        float* dst = paged_f32_dest(a, f, warp, kHd, sum[0] > 0.0f ? top[0] + log2f(sum[0]) : -INFINITY, lane == 0);
+        const float inv = sum[0] == 0.0f ? 0.0f : 1.0f / sum[0];
+        float* dst = paged_f32_dest(a, f, warp, kHd, sum[0] == 0.0f ? -INFINITY : top[0] + log2f(sum[0]), lane == 0);
 #pragma unroll
         for (int c = 0; c < kOc; ++c)
           *reinterpret_cast<float2*>(dst + c * 64 + lane * 2) = make_float2(o[0][2 * c] * inv, o[0][2 * c + 1] * inv);
@@ -722,8 +722,8 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(const __grid_constant
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= f.rows) continue;
-      const float inv = sum[i] > 0.0f ? 1.0f / sum[i] : 0.0f;
-      float* dst = paged_f32_dest(a, f, r, kHd, sum[i] > 0.0f ? top[i] + log2f(sum[i]) : -INFINITY, tx == 0);
+      const float inv = sum[i] == 0.0f ? 0.0f : 1.0f / sum[i];
+      float* dst = paged_f32_dest(a, f, r, kHd, sum[i] == 0.0f ? -INFINITY : top[i] + log2f(sum[i]), tx == 0);
 #pragma unroll
       for (int c = 0; c < kOc; ++c)
         *reinterpret_cast<float4*>(dst + c * 64 + tx * 4) =

@@ -160,10 +160,11 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;                             // A, B
-  uint8_t* sKV = smem + kRows / 128 * C::kBytes;            // ring of K and V blocks
+  uint8_t* sKV = smem + kRows / 128 * C::kBytes;  // ring of K and V blocks
   uint8_t* sStage = sKV + ST * C::kBytes;         // epilogue staging
   __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], frag_full[kPaFrags], frag_empty[kPaFrags];
-  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], o_done[2], half_full, half_empty, v_last, v_tail[2], turn[2][4];
+  __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], o_done[2];
+  __shared__ __align__(8) uint64_t half_full, half_empty, v_last, v_tail[2], turn[2][4];
   __shared__ PagedFrag s_frag[kPaFrags];
   __shared__ float s_half[128][2];                // split: maximum and sum of B's half, per row
   __shared__ uint32_t tmem_base;
@@ -558,10 +559,11 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       if (warp_on) {
         const long long rows_all = (long long)a.b.n_tokens * a.n_heads, row = (long long)tok * a.n_heads + head;
         const bool final = whole && a.b.prefix_len == 0;
-        const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
-        const float l2 = l_run > 0.0f ? m_run + log2f(l_run) : -INFINITY;
-        w0 = l_run > 0.0f ? w0 * inv : 0.0f;
-        w1 *= inv;
+        // (a sum of 0: no visible key; not a number stays that)
+        const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+        const float l2 = l_run == 0.0f ? -INFINITY : m_run + log2f(l_run);
+        w0 *= inv;
+        w1 = both ? w1 * inv : 0.0f;
         // where the row goes, as bytes
         char* dst = nullptr;
         if (r < n_rows) {
@@ -579,7 +581,9 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         uint8_t* stage = sStage + warp * kPaStage;
         const int cols = final ? 64 : 32;            // columns of 128 bytes
         const int live = min(32, n_rows - wt * 32);
-        const bool add_b = __any_sync(0xffffffffu, w1 != 0.0f);
+        // (by the piece, never by values: rows past the end may hold anything, and
+        // past B's columns there is no tensor memory)
+        const bool add_b = both;
 #pragma unroll 1
         for (int q = 0; q < kHd; q += 16) {
           uint32_t o[16];

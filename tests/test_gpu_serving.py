@@ -388,6 +388,37 @@ def test_attention_with_rising_and_large_scores(new, dtype):
     check_attention(b, q, False, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("new", [[1, 1], [40, 200]])
+def test_a_query_that_is_not_a_number_stays_its_own_problem(dtype, new):
+    b = Batch(17, dtype, 2, 64, 16, new, [300, 9], 50)
+    q = randn(gen(9), b.rows, 6, 64, dtype=dtype)
+    good, good_lse = check_attention(b, q, True, dtype)
+    bad = q.clone()
+    bad[0, 3, 7] = float("nan")
+    bad[b.rows - 1, 0, 63] = float("nan")
+    out, lse = torch.empty_like(q), torch.empty(b.rows, 6, device="cuda")
+    dg.paged_attention(b.cache, b.batch, bad, out, lse=lse)
+    hit = torch.zeros(b.rows, 6, dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[b.rows - 1, 0] = True
+    assert torch.all(torch.isnan(out[hit].float())) and torch.all(torch.isnan(lse[hit]))
+    assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[~hit], good_lse[~hit])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_rows_left_by_a_bad_sequence_reach_no_other(dtype):
+    # ragged pieces follow full ones on the same CTA, and find their rows in place
+    b = Batch(18, dtype, 2, 64, 32, [520] * 8 + [130, 37, 1, 130, 9, 260] * 6, [700] * 44, 0)
+    q = randn(gen(10), b.rows, 6, 64, dtype=dtype)
+    good, good_lse = check_attention(b, q, False, dtype)
+    bad = q.clone()
+    bad[:8 * 520] = float("nan")
+    out, lse = torch.empty_like(q), torch.empty(b.rows, 6, device="cuda")
+    dg.paged_attention(b.cache, b.batch, bad, out, lse=lse, causal=False)
+    assert torch.all(torch.isnan(out[:8 * 520].float())) and torch.all(torch.isnan(lse[:8 * 520]))
+    assert torch.equal(out[8 * 520:], good[8 * 520:]) and torch.equal(lse[8 * 520:], good_lse[8 * 520:])
+
+
 def test_attention_repeats_bit_for_bit_whatever_the_workspace_holds():
     b = Batch(9, BF, 2, 128, 64, [256, 1, 30], [3000, 700, 0], 500)
     q = randn(gen(8), b.rows, 8, 128, dtype=BF)
