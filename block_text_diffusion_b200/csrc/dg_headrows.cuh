@@ -238,18 +238,25 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // token, not to the head, so they are formed once a batch, and two pairs go
 // through one packed instruction.
 //
-// Bound by memory when there are many tokens (26B heads, 8192 tokens: one
-// read and one write of 50 MB each), by the launch and two dependent reads
-// when there are few.  Forming the gains and phases for every head took 1340
-// instructions a warp and 41 us; this form takes fewer than half.
+// A block is one warp: nothing is shared between warps, and a slot is free as
+// soon as its warp ends, where the block of 8 waited for its last one (26B
+// heads: 16 canvases of 256 tokens 28.7 to 26.6 us, an append of 8192 prompt
+// tokens 61.4 to 55.3, of 64 single tokens 8.2 to 6.7; blocks of 4 and 2 lie
+// between).  What comes from memory without the position (frequencies, gains)
+// is asked for before the sequence is looked up, so the chain of dependent
+// loads is the batch's alone.
+//
+// Many tokens: 4.6 TB/s (101 MB, 22.0 us among others) and 5.3 (268 MB, 51.0 us),
+// the instructions (1320 a warp) at 16 warps an SM being what is left; few: the
+// launch and two dependent reads (3.3 us).
 template <typename T, int kGroups, bool kInter>
-__global__ void __launch_bounds__(256, 2) k_head_rows(const __grid_constant__ HeadRowsArgs a, int lph_shift,
-                                                       unsigned warps_per_token, int batches_per_warp) {
+__global__ void __launch_bounds__(32, 16) k_head_rows(const __grid_constant__ HeadRowsArgs a, int lph_shift,
+                                                      unsigned warps_per_token, int batches_per_warp) {
   constexpr int N = Chunk<T>::kN;
-  __shared__ __align__(16) float s_cos[8][128], s_sin[8][128];
+  __shared__ __align__(16) float s_cos[128], s_sin[128];
   pdl_enter();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned w = blockIdx.x * 8u + warp;
+  const int lane = threadIdx.x;
+  const unsigned w = blockIdx.x;
   const int t = (int)(warps_per_token == 1 ? w : w / warps_per_token);
   if (t >= a.n_tokens) return;
   const int lph = 1 << lph_shift, hpw = 32 >> lph_shift;   // lanes a head, heads a group
@@ -296,21 +303,34 @@ __global__ void __launch_bounds__(256, 2) k_head_rows(const __grid_constant__ He
       xa[i] = at[ca];
       xb[i] = at[cb];
     }
+    const uint4* gain = reinterpret_cast<const uint4*>(kind == 0 ? a.q_gain : a.k_gain);
+    const bool gained = kind < 2 && a.norm && gain;
+    uint4 gain_a = {}, gain_b = {};
+    if (gained) {
+      gain_a = gain[ca];
+      gain_b = gain[cb];
+    }
     if (!have_spot) {
       have_spot = true;
+      double freq[4];                                  // (rp <= 128)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) freq[i] = lane + 32 * i < rp ? a.inv_freq[lane + 32 * i] : 0.0;
       spot = token_spot(a, t);
       if (!spot.live) return;
       if (rp > 0 && kind < 2) {
-        for (int p = lane; p < rp; p += 32)
-          turn_sincos(spot.pos, a.inv_freq[p], a.amplitude, s_cos[warp][p], s_sin[warp][p]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = lane + 32 * i;
+          if (p < rp) turn_sincos(spot.pos, freq[i], a.amplitude, s_cos[p], s_sin[p]);
+        }
         __syncwarp();
         const int pa = kInter ? ca * (N / 2) : j * N, pb = kInter ? cb * (N / 2) : j * N + N / 2;
 #pragma unroll
         for (int e = 0; e < N / 2; e += 2) {
-          const float2 c0 = *reinterpret_cast<const float2*>(&s_cos[warp][pa + e]),
-                       c1 = *reinterpret_cast<const float2*>(&s_cos[warp][pb + e]),
-                       s0 = *reinterpret_cast<const float2*>(&s_sin[warp][pa + e]),
-                       s1 = *reinterpret_cast<const float2*>(&s_sin[warp][pb + e]);
+          const float2 c0 = *reinterpret_cast<const float2*>(&s_cos[pa + e]),
+                       c1 = *reinterpret_cast<const float2*>(&s_cos[pb + e]),
+                       s0 = *reinterpret_cast<const float2*>(&s_sin[pa + e]),
+                       s1 = *reinterpret_cast<const float2*>(&s_sin[pb + e]);
           c[e] = c0.x; c[e + 1] = c0.y; c[N / 2 + e] = c1.x; c[N / 2 + e + 1] = c1.y;
           s[e] = s0.x; s[e + 1] = s0.y; s[N / 2 + e] = s1.x; s[N / 2 + e + 1] = s1.y;
         }
@@ -347,10 +367,9 @@ __global__ void __launch_bounds__(256, 2) k_head_rows(const __grid_constant__ He
     float2 uc[N / 2], vs[N / 2], vc[N / 2], us[N / 2];
     {
       float ga[N], gb[N];
-      const uint4* gain = reinterpret_cast<const uint4*>(kind == 0 ? a.q_gain : a.k_gain);
-      if (a.norm && gain) {
-        Chunk<T>::unpack(gain[ca], ga);
-        Chunk<T>::unpack(gain[cb], gb);
+      if (gained) {
+        Chunk<T>::unpack(gain_a, ga);
+        Chunk<T>::unpack(gain_b, gb);
       } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) ga[e] = gb[e] = 1.0f;

@@ -180,14 +180,14 @@ dg_status run_head_rows(const HeadRowsArgs& a, cudaStream_t s) {
   const bool many = (long long)a.n_tokens * batches(1) > kSMs * 32;
   const int nb = batches(many ? 4 : 1), per = many ? nb : 1;
   const int wpt = (nb + per - 1) / per;
-  const long long blocks = ((long long)a.n_tokens * wpt + 7) / 8;
-  if (blocks >= (1ll << 28)) return DG_ERR_INVALID_ARG;   // (warps are counted in 32 bits)
+  const long long blocks = (long long)a.n_tokens * wpt;
+  if (blocks >= (1ll << 31)) return DG_ERR_INVALID_ARG;   // (blocks of one warp, counted in 32 bits)
   const unsigned g = (unsigned)blocks;
   if (a.interleaved)
-    return done(many ? launch(k_head_rows<T, 4, true>, g, 256, 0, s, a, shift, (unsigned)wpt, per)
-                     : launch(k_head_rows<T, 1, true>, g, 256, 0, s, a, shift, (unsigned)wpt, per));
-  return done(many ? launch(k_head_rows<T, 4, false>, g, 256, 0, s, a, shift, (unsigned)wpt, per)
-                   : launch(k_head_rows<T, 1, false>, g, 256, 0, s, a, shift, (unsigned)wpt, per));
+    return done(many ? launch(k_head_rows<T, 4, true>, g, 32, 0, s, a, shift, (unsigned)wpt, per)
+                     : launch(k_head_rows<T, 1, true>, g, 32, 0, s, a, shift, (unsigned)wpt, per));
+  return done(many ? launch(k_head_rows<T, 4, false>, g, 32, 0, s, a, shift, (unsigned)wpt, per)
+                   : launch(k_head_rows<T, 1, false>, g, 32, 0, s, a, shift, (unsigned)wpt, per));
 }
 
 dg_status run_head_rows(int dtype, HeadRowsArgs& a, cudaStream_t s) {
