@@ -334,6 +334,14 @@ ATTN = [
     (4, 1, 128, 64, True, [100, 9], [-60, 200], 37),     # rows that see the prefix alone
     (2, 1, 64, 16, False, [3, 5, 2], [-3, 20, -2], 0),   # sequences without a key
     (8, 8, 128, 64, True, [1] * 200, [i * 7 % 180 for i in range(200)], 0),
+    # prefixes that end inside a block and a page, before few and many rows
+    (4, 2, 128, 16, True, [1], [37], 129),
+    (4, 2, 128, 16, True, [1], [200], 300),
+    (2, 1, 64, 64, True, [2, 1], [127, 900], 3),
+    (4, 1, 64, 32, False, [100], [150], 77),
+    (16, 1, 128, 64, True, [64, 40], [0, 3], 1000),
+    (8, 8, 128, 128, True, [200, 57, 0, 256], [33, 0, 4, 512], 513),
+    (2, 2, 64, 16, True, [130, 300], [0, 1], 16),
     (8, 2, 128, 32, True, [30] * 60, [300] * 60, 0),     # several joined halves of 120 rows in one CTA
     (130, 1, 64, 16, True, [3, 1], [9, 200], 20),        # more query heads than a half tile has rows
     (2, 2, 64, 16, True, [1, 0, 3] * 500, [5, 9, 0] * 500, 3),   # more sequences than a warp looks at at once
