@@ -79,9 +79,10 @@ struct PagedFrag {
 // Starting and ending a tile (query rows in, first scores, output) in units of
 // a key block.  Measured on 8 canvases behind a 32768-token prefix (256-row
 // tiles): 2 units 285 us, 3 to 5 263 us; ragged causal prompts 129, 128.5,
-// 125 and 123 us for 2, 3, 4 and 5; on 64 single tokens (128-row tiles): 3
-// units 87.7 us, 4 90.0 us.
-constexpr int paged_tile_cost(int rows) { return rows == 256 ? 5 : rows == 128 ? 3 : 2; }
+// 125 and 123 us for 2, 3, 4 and 5; 64 single tokens (128-row tiles, bound by
+// memory, which a tile's start and end hardly hold up): 4 units 90.0 us,
+// 3 86.7, 2 85.1, 1 84.9.
+constexpr int paged_tile_cost(int rows) { return rows == 256 ? 5 : 2; }
 
 template <int kRows, int kBlk>
 struct PagedWalk {

@@ -275,7 +275,7 @@ def test_walk_covers_every_block_once(L, tile):
         per = {}
         for f in frags:
             per.setdefault(f["cta"], []).append(f)
-        fixed = {256: 5, 128: 3, 64: 2}[tile]            # a tile's start and end, counted in blocks
+        fixed = {256: 5, 128: 2, 64: 2}[tile]            # a tile's start and end, counted in blocks
         total = sum(nb + fixed for _, nb in want.values())
         share = -(-total // 148)
         for fs in per.values():
