@@ -363,44 +363,73 @@ __device__ __forceinline__ PagedDest paged_dest(const PagedAttnArgs& a, const Pa
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // Joins the pieces of every row: own keys first, then the prefix, each in key
-// order.  16 lanes read a piece, four pieces at a time.  kShare groups of 16
-// lanes share a row: 1 where there are rows enough for every lane, 16 (the
-// block) for a few rows, which a long context may have cut into 148 pieces.
+// order.  A block looks at `per_block` rows (at most 64), lists those the main
+// kernel did not finish (without a prefix most are), and its 16 groups of 16
+// lanes take them in turn, kBatch pieces at a time.  With few rows a block has
+// one, and its groups (kShare = 16) share the pieces: a long context may have
+// cut it into 148.
+//
+// Bound by the chain batch -> meta -> pieces and its instructions (41 % of the
+// issue slots, 33 % of the memory rate).  Listing the open rows for the whole
+// block, dividing and clamping once a row in the listing, and one reference for
+// a batch of pieces took ragged causal prompts from 18.5 to 11.4 us (a sixth of
+// their rows is cut), 8 canvases behind a shared prompt from 16.5 to 14.4.
+// Blocks an SM x pieces in flight: 4 x 4 as good as 5 x 2 and 3 x 4; with one or
+// two pieces at 8 blocks the registers spill (91 and 105 us for the whole call
+// against 85).
+constexpr int kJoinRows = 64;
+
 template <typename T, int kHd, int kShare>
-__global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, int grid_main) {
+__global__ void __launch_bounds__(256, kShare > 1 ? 1 : 4)
+k_paged_join(const __grid_constant__ PagedAttnArgs a, int row_shift, int grid_main, int per_block) {
   constexpr int kPer = kHd / 16, kBatch = 4;   // columns a lane, pieces in flight
   __shared__ float s_acc[kShare > 1 ? 16 : 1][kHd], s_ref[16], s_sum[16];
+  __shared__ int4 s_job[kJoinRows];       // row, first slot of each part, pieces of part 0 and (from bit 16) 1
+  __shared__ long long s_dst[kJoinRows];
+  __shared__ int s_n;
   pdl_wait();
   const int grp = threadIdx.x >> 4, lane = threadIdx.x & 15;
   const int share = kShare > 1 ? grp : 0;
   const long long rows = (long long)a.b.n_tokens * a.n_heads;
   const int parts = a.b.prefix_len > 0 ? 2 : 1;
-  const int lo = a.b.n_seqs > 0 ? a.b.cu_q[0] : 0, hi = a.b.n_seqs > 0 ? a.b.cu_q[a.b.n_seqs] : 0;
-  const long long row_lo = (long long)lo * a.n_heads, row_hi = lmin((long long)hi * a.n_heads, rows);
-  // Without a prefix most rows are finished already.  Where a group has several
-  // rows its lanes look at their meta at once and it goes on to those that are
-  // not (chunks of as many rows as a group has, so none waits on another's).
-  const long long groups = (long long)gridDim.x * 16 / kShare;
-  const int chunk = kShare > 1 || parts == 2 ? 1 : (int)lmin(16, (rows + groups - 1) / groups);
-  for (long long c0 = ((long long)blockIdx.x * 16 + grp) / kShare * chunk; c0 < rows; c0 += groups * chunk) {
-   unsigned todo = 1;
-   if (chunk > 1) {
-     const long long mine = c0 + lane;
-     const bool open = lane < chunk && mine >= row_lo && mine < row_hi && a.meta[mine].x >= 0;
-     todo = __ballot_sync(0xffffu << (threadIdx.x & 16), open) >> (threadIdx.x & 16) & 0xffffu;
-   }
-   for (; todo; todo &= todo - 1) {
-    const long long row = c0 + __ffs(todo) - 1;
-    if (row < row_lo || row >= row_hi) continue;
-    const int tok = (int)((unsigned)row / (unsigned)a.n_heads), head = (int)row - tok * a.n_heads;
-    const int2 m0 = a.meta[row], m1 = parts == 2 ? a.meta[rows + row] : make_int2(0, 0);
-    if (m0.x < 0) continue;   // written by the main kernel
-    // first CTA, row in the tile, pieces of each part (what a row no tile
-    // covered finds here still stays in the workspace)
-    const int cta0 = min(max(m0.x, 0), grid_main - 1), cta1 = min(max(m1.x, 0), grid_main - 1);
-    const int r0 = m0.y & (kRows - 1), r1 = m1.y & (kRows - 1);
-    const int n0 = 1 + min(max(m0.y / kRows, 0), grid_main - 1 - cta0);
-    const int n = n0 + (parts == 2 ? 1 + min(max(m1.y / kRows, 0), grid_main - 1 - cta1) : 0);
+  if (threadIdx.x < 32) {
+    const int lo = a.b.n_seqs > 0 ? a.b.cu_q[0] : 0, hi = a.b.n_seqs > 0 ? a.b.cu_q[a.b.n_seqs] : 0;
+    const long long row_lo = (long long)lo * a.n_heads, row_hi = lmin((long long)hi * a.n_heads, rows);
+    int2 m0[kJoinRows / 32], m1[kJoinRows / 32];
+#pragma unroll
+    for (int h = 0; h < kJoinRows / 32; ++h) {
+      const int i = 32 * h + threadIdx.x;
+      const long long row = (long long)blockIdx.x * per_block + i;
+      const bool in = i < per_block && row >= row_lo && row < row_hi;
+      m0[h] = in ? a.meta[row] : make_int2(-1, 0);       // (-1: written by the main kernel)
+      m1[h] = in && parts == 2 ? a.meta[rows + row] : make_int2(0, 0);
+    }
+    int n = 0;
+#pragma unroll
+    for (int h = 0; h < kJoinRows / 32; ++h) {
+      const unsigned open = __ballot_sync(0xffffffffu, m0[h].x >= 0);
+      const int at = n + __popc(open & ((1u << threadIdx.x) - 1));
+      if (m0[h].x >= 0) {
+        // first CTA, row in the tile, later CTAs of each part (what a row no
+        // tile covered finds here still stays in the workspace)
+        const int cta0 = min(m0[h].x, grid_main - 1), cta1 = min(max(m1[h].x, 0), grid_main - 1);
+        const int n0 = 1 + min(max(m0[h].y >> row_shift, 0), grid_main - 1 - cta0);
+        const int n1 = parts == 1 ? 0 : 1 + min(max(m1[h].y >> row_shift, 0), grid_main - 1 - cta1);
+        const int i = 32 * h + threadIdx.x, mask = (1 << row_shift) - 1;
+        s_job[at] = make_int4(i, (cta0 << row_shift) + (m0[h].y & mask), (cta1 << row_shift) + (m1[h].y & mask),
+                              n0 | n1 << 16);
+        const unsigned row = (unsigned)blockIdx.x * per_block + i, tok = row / (unsigned)a.n_heads;
+        s_dst[at] = tok * a.o_ts + (row - tok * a.n_heads) * a.o_hs;
+      }
+      n += __popc(open);
+    }
+    if (threadIdx.x == 0) s_n = n;
+  }
+  __syncthreads();
+  for (int k = kShare > 1 ? 0 : grp; k < s_n; k += kShare > 1 ? 1 : 16) {
+    const int4 job = s_job[k];
+    const long long row = (long long)blockIdx.x * per_block + job.x;
+    const int n0 = job.w & 0xffff, n = n0 + (job.w >> 16);
     float acc[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
@@ -410,34 +439,40 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, 
       float lse[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        int i = i0 + u * kShare;
+        const int i = i0 + u * kShare;
         lse[u] = -INFINITY;
         if (i >= n) continue;
-        const int p = i >= n0;
-        i -= p ? n0 : 0;
-        const long long at = (long long)((p ? cta1 : cta0) + i) * kRows + (p ? r1 : r0);
-        const float* o = i == 0 ? a.part_o + (p * rows + row) * kHd : a.slot_o + at * kHd;
-        lse[u] = i == 0 ? a.part_lse[p * rows + row] : a.slot_lse[at];
+        // a part's first piece lies in the row's place, the others in their CTA's slot
+        const bool p = i >= n0, slot = i != 0 && i != n0;
+        const long long at = slot ? (p ? job.z : job.y) + ((p ? i - n0 : i) << row_shift) : p ? rows + row : row;
+        const float* o = (slot ? a.slot_o : a.part_o) + at * kHd;
+        lse[u] = (slot ? a.slot_lse : a.part_lse)[at];
 #pragma unroll
         for (int c = 0; c < kPer / 4; ++c) v[u][c] = *reinterpret_cast<const float4*>(o + c * 64 + lane * 4);
       }
+      float up = top;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) up = fmaxf(up, lse[u]);
+      const float ref = up == -INFINITY ? 0.0f : up, w0 = exp2f(top - ref);
+      top = up;
+      sum *= w0;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) acc[c] *= w0;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        if (lse[u] == -INFINITY) continue;
-        const float up = fmaxf(top, lse[u]);
-        const float w0 = top == -INFINITY ? 0.0f : exp2f(top - up), w1 = exp2f(lse[u] - up);
-        top = up;
-        sum = sum * w0 + w1;
+        if (lse[u] == -INFINITY) continue;    // (no piece, or no visible key)
+        const float w = exp2f(lse[u] - ref);
+        sum += w;
 #pragma unroll
         for (int c = 0; c < kPer / 4; ++c) {
-          acc[c * 4] = acc[c * 4] * w0 + v[u][c].x * w1;
-          acc[c * 4 + 1] = acc[c * 4 + 1] * w0 + v[u][c].y * w1;
-          acc[c * 4 + 2] = acc[c * 4 + 2] * w0 + v[u][c].z * w1;
-          acc[c * 4 + 3] = acc[c * 4 + 3] * w0 + v[u][c].w * w1;
+          acc[c * 4] += v[u][c].x * w;
+          acc[c * 4 + 1] += v[u][c].y * w;
+          acc[c * 4 + 2] += v[u][c].z * w;
+          acc[c * 4 + 3] += v[u][c].w * w;
         }
       }
     }
-    T* dst = (T*)a.out + (long long)tok * a.o_ts + (long long)head * a.o_hs;
+    T* dst = (T*)a.out + s_dst[k];
     if (kShare == 1) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -446,7 +481,7 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, 
                   acc[c * 4 + 3] * inv);
       if (a.lse && lane == 0) a.lse[row] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
     } else {
-      // (the whole block is on one row: the branches above were uniform)
+      // (the whole block is on its one row: the branches above were uniform)
       __syncthreads();
 #pragma unroll
       for (int c = 0; c < kPer / 4; ++c)
@@ -471,7 +506,6 @@ __global__ void __launch_bounds__(256) k_paged_join(PagedAttnArgs a, int kRows, 
         if (a.lse && threadIdx.x == 0) a.lse[row] = z == 0.0f ? -INFINITY : (ref + log2f(z)) * kLn2;
       }
     }
-   }
   }
 }
 

@@ -221,10 +221,13 @@ PagedSpace paged_space(int64_t n_tokens, int64_t n_heads, int64_t head_dim, bool
 template <typename T, int kHd>
 dg_status run_join(const PagedAttnArgs& a, int tile, cudaStream_t s) {
   const long long rows = (long long)a.b.n_tokens * a.n_heads;
+  int shift = 0;   // (tiles have 2^shift rows)
+  while ((1 << shift) < tile) ++shift;
   // a block per row while the rows do not fill the SMs
-  if (rows <= kSMs) return done(launch(k_paged_join<T, kHd, 16>, (unsigned)rows, 256, 0, s, a, tile, (int)kSMs));
-  const unsigned blocks = (unsigned)std::min<long long>((rows + 15) / 16, kSMs * 8);
-  return done(launch(k_paged_join<T, kHd, 1>, blocks, 256, 0, s, a, tile, (int)kSMs));
+  if (rows <= kSMs) return done(launch(k_paged_join<T, kHd, 16>, (unsigned)rows, 256, 0, s, a, shift, (int)kSMs, 1));
+  const int per_block = (int)std::min<long long>(kJoinRows, (rows / (kSMs * 5) + 16) / 16 * 16);
+  return done(launch(k_paged_join<T, kHd, 1>, (unsigned)((rows + per_block - 1) / per_block), 256, 0, s, a, shift,
+                     (int)kSMs, per_block));
 }
 
 template <int kHd, bool kNarrow>
