@@ -382,7 +382,7 @@ constexpr int kJoinRows = 64;
 template <typename T, int kHd, int kShare>
 __global__ void __launch_bounds__(256, kShare > 1 ? 1 : 4)
 k_paged_join(const __grid_constant__ PagedAttnArgs a, int row_shift, int grid_main, int per_block) {
-  constexpr int kPer = kHd / 16, kBatch = 4;   // columns a lane, pieces in flight
+  constexpr int kPer = kHd / 16, kBatch = kShare > 1 ? 8 : 4;   // columns a lane, pieces in flight
   __shared__ float s_acc[kShare > 1 ? 16 : 1][kHd], s_ref[16], s_sum[16];
   __shared__ int4 s_job[kJoinRows];       // row, first slot of each part, pieces of part 0 and (from bit 16) 1
   __shared__ long long s_dst[kJoinRows];
