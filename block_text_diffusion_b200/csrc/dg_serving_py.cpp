@@ -36,7 +36,7 @@ struct Refused {};   // a Python exception is set
 }
 
 // Interned attribute names.
-#define DG_NAMES(X) X(_at) X(index) X(q_gain) X(k_gain) X(_words) X(cuda_stream) X(device)
+#define DG_NAMES(X) X(_at) X(index) X(inv_freq) X(q_gain) X(k_gain) X(k) X(v) X(_words) X(cuda_stream) X(device)
 #define X(n) PyObject* s_##n;
 DG_NAMES(X)
 #undef X
@@ -65,9 +65,8 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 const char* type_name(at::ScalarType t) { return t == at::kBFloat16 ? "bfloat16" : t == at::kFloat ? "float32" : "int32"; }
 
 // A tensor of a type and shape on a device.
-const at::Tensor& check(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, int index,
+const at::Tensor& check(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, int index,
                         bool contiguous) {
-  const at::Tensor& t = tensor(o, name);
   if (t.scalar_type() != type || t.sizes() != shape || !t.is_cuda() || t.get_device() != index ||
       (contiguous && !t.is_contiguous()) || t.layout() != at::kStrided) {
     Ref want(PyTuple_New((Py_ssize_t)shape.size()));
@@ -78,12 +77,18 @@ const at::Tensor& check(PyObject* o, const char* name, at::ScalarType type, at::
   return t;
 }
 
+const at::Tensor& check(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, int index,
+                        bool contiguous) {
+  return check(tensor(o, name), name, type, shape, index, contiguous);
+}
+
 // [tokens, heads, head_dim] with contiguous components.
 dg_heads rows(PyObject* o, const char* name, at::ScalarType type, int64_t tokens, int64_t heads, int64_t dim, int index,
               bool out) {
   const int64_t shape[3] = {tokens, heads, dim};
   const at::Tensor& t = check(o, name, type, at::IntArrayRef(shape, 3), index, false);
-  const int64_t st = t.stride(0), sh = t.stride(1), n = tokens * heads;
+  // (the stride of a dimension of one entry means nothing)
+  const int64_t st = tokens == 1 ? 0 : t.stride(0), sh = heads == 1 ? 0 : t.stride(1), n = tokens * heads;
   if (t.stride(2) != 1 && dim > 1 && n > 0) refuse("%s: the components of a head must be contiguous", name);
   if (out && n > 0) {
     // rows that share memory would be written by several warps at once
@@ -100,19 +105,29 @@ at::ScalarType model_type(const at::Tensor& t) {
   return t.scalar_type();
 }
 
+// A tensor whose address an argument object noted when it was made: its memory
+// may have been replaced since (a module moved to another type or device).
+const at::Tensor& held(const Ref& r, const char* name, const void* noted) {
+  const at::Tensor& t = tensor(r.p, name);
+  if (t.data_ptr() != noted) refuse("%s has other memory than when it was given: make the argument object anew", name);
+  return t;
+}
+
 const dg_rope* rope_of(PyObject* o, int index) {
   if (o == Py_None) return nullptr;
-  if (attr_int(o, s_index) != index) refuse("inv_freq must be on cuda:%d", index);
-  return reinterpret_cast<const dg_rope*>(attr_int(o, s__at));
+  Ref freq(PyObject_GetAttr(o, s_inv_freq));   // (only a Rope has it)
+  const dg_rope* r = reinterpret_cast<const dg_rope*>(attr_int(o, s__at));
+  if (held(freq, "inv_freq", r->inv_freq).get_device() != index) refuse("inv_freq must be on cuda:%d", index);
+  return r;
 }
 
 const dg_head_norm* norm_of(PyObject* o, at::ScalarType type, int64_t dim, int index) {
   if (o == Py_None) return nullptr;
-  for (PyObject* name : {s_q_gain, s_k_gain}) {
-    Ref gain(PyObject_GetAttr(o, name));
-    if (gain.p != Py_None) check(gain.p, "a gain", type, at::IntArrayRef(&dim, 1), index, true);
-  }
-  return reinterpret_cast<const dg_head_norm*>(attr_int(o, s__at));
+  Ref q_gain(PyObject_GetAttr(o, s_q_gain)), k_gain(PyObject_GetAttr(o, s_k_gain));   // (only a HeadNorm has them)
+  const dg_head_norm* h = reinterpret_cast<const dg_head_norm*>(attr_int(o, s__at));
+  if (q_gain.p != Py_None) check(held(q_gain, "q_gain", h->q_gain), "q_gain", type, at::IntArrayRef(&dim, 1), index, true);
+  if (k_gain.p != Py_None) check(held(k_gain, "k_gain", h->k_gain), "k_gain", type, at::IntArrayRef(&dim, 1), index, true);
+  return h;
 }
 
 struct Cache {
@@ -122,7 +137,10 @@ struct Cache {
 };
 Cache cache_of(PyObject* o) {
   Cache r;
+  Ref k(PyObject_GetAttr(o, s_k)), v(PyObject_GetAttr(o, s_v));   // (only a PagedKV has them)
   r.c = reinterpret_cast<const dg_paged_kv*>(attr_int(o, s__at));
+  held(k, "the cache's k", r.c->k);
+  held(v, "the cache's v", r.c->v);
   r.index = (int)attr_int(o, s_index);
   r.type = r.c->dtype == DG_BF16 ? at::kBFloat16 : at::kFloat;
   return r;

@@ -1,11 +1,13 @@
 """Serving operators over a paged key/value cache (include/dg.h).
 
 Argument checks and marshalling (in C++, csrc/dg_serving_py.cpp: the calls are
-short); the work is in libdg.so.  Tensors may be
-views with any token and head stride as long as the components of a head are
-contiguous.  Every call is asynchronous on `stream` (default: the current
-stream of the tensors' device), allocates nothing but a workspace the caller
-did not bring, and can be captured into a CUDA graph.
+short); the work is in libdg.so.  Tensors may be views with any token and head
+stride as long as the components of a head are contiguous.  Every call is
+asynchronous on `stream` (default: the current stream of the tensors' device),
+allocates nothing but a workspace the caller did not bring, and can be captured
+into a CUDA graph.  Nothing is recorded for a backward pass.  The argument
+objects note the addresses of their tensors, so they cannot be changed after
+they were made; the tensors' contents may.
 
     cache = PagedKV(k_pages, v_pages)                   # [n_pages, Hkv, page, hd]
     batch = PagedBatch(cu_q, kv_lens, page_table)       # device int32
@@ -98,7 +100,16 @@ def _dtype_code(dtype):
     return 1 if dtype == torch.bfloat16 else 0
 
 
-class Rope:
+class _Fixed:
+    """What a call reads was noted when the object was made, so nothing is reassigned later."""
+
+    def __setattr__(self, name, value):
+        if "_fixed" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: make another {type(self).__name__}")
+        self.__dict__[name] = value
+
+
+class Rope(_Fixed):
     """Position rotation: pair j of a head turns by position * inv_freq[j].
 
     inv_freq: float64 device tensor [rot_dim / 2] (see rope_frequencies); the
@@ -114,9 +125,10 @@ class Rope:
         self.rot_dim = 2 * inv_freq.numel()
         self._c = _Rope(inv_freq.data_ptr(), self.rot_dim, int(bool(interleaved)), float(amplitude))
         self._at = ctypes.addressof(self._c)
+        self._fixed = True
 
 
-class HeadNorm:
+class HeadNorm(_Fixed):
     """RMSNorm of each head: x / sqrt(mean(x^2) + eps) * gain (gains [head_dim], None: ones)."""
 
     def __init__(self, eps=1e-6, q_gain=None, k_gain=None):
@@ -125,6 +137,7 @@ class HeadNorm:
         self._c = _HeadNorm(1, float(eps), None if q_gain is None else q_gain.data_ptr(),
                             None if k_gain is None else k_gain.data_ptr())
         self._at = ctypes.addressof(self._c)
+        self._fixed = True
 
 
 def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=None, beta_fast=32.0,
@@ -168,7 +181,7 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, origina
     return out, 0.1 * math.log(factor) + 1.0
 
 
-class PagedKV:
+class PagedKV(_Fixed):
     """A paged cache: keys and values [n_pages, n_kv_heads, page_size, head_dim],
     contiguous, page_size a power of two from 16 to 256."""
 
@@ -185,6 +198,7 @@ class PagedKV:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self._c = _PagedKV(k.data_ptr(), v.data_ptr(), code, self.n_pages, self.n_kv_heads, page, self.head_dim)
         self._at = ctypes.addressof(self._c)
+        self._fixed = True
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype, device="cuda"):
@@ -194,7 +208,7 @@ class PagedKV:
         return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device))
 
 
-class PagedBatch:
+class PagedBatch(_Fixed):
     """A ragged batch over a paged cache: sequence b has the token rows
     cu_q[b] .. cu_q[b+1] - 1 as its newest tokens and kv_lens[b] tokens of its
     own in the cache, those included, in the pages page_table[b].  prefix_len
@@ -224,6 +238,7 @@ class PagedBatch:
                        max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
                        prefix_pages.data_ptr() if prefix_len else 0, int(prefix_len),
                        prefix_pages.numel() if prefix_len else 0)
+        self._fixed = True
 
 
 def qk_norm_rope(q, k, positions, q_out, k_out, rope=None, norm=None, stream=None):

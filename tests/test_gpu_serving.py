@@ -580,6 +580,45 @@ def test_binding_refuses_mismatched_tensors():
         dg.paged_attention(b.cache, b.batch, x, q)
 
 
+def test_argument_objects_stay_what_they_were():
+    b = Batch(52, BF, 2, 64, 16, [1, 1], [5, 5])
+    q, k = randn(gen(1), 2, 4, 64, dtype=BF), randn(gen(2), 2, 2, 64, dtype=BF)
+    w, _ = freqs(64)
+    pos, gain = i32([0, 1]), torch.ones(64, dtype=BF, device="cuda")
+    rope, norm = dg.Rope(w), dg.HeadNorm(1e-6, gain, gain)
+    for thing, name in ((rope, "inv_freq"), (norm, "q_gain"), (b.cache, "k"), (b.batch, "kv_lens"), (b.batch, "prefix_len")):
+        with pytest.raises(AttributeError):
+            setattr(thing, name, getattr(thing, name))
+    # one kind of object in another's place
+    for f in (lambda: dg.qk_norm_rope(q, k, pos, q, k, rope=b.cache), lambda: dg.qk_norm_rope(q, k, pos, q, k, norm=rope),
+              lambda: dg.paged_attention(rope, b.batch, q, q), lambda: dg.paged_attention(b.cache, norm, q, q)):
+        with pytest.raises(AttributeError):
+            f()
+    # tensors that got other memory
+    old = [t.data for t in (gain, w, b.k)]   # (kept: the noted addresses stay allocated)
+    want = q.clone()
+    gain.data = gain.clone()
+    w.data = w.clone()
+    b.k.data = b.k.clone()
+    for f in (lambda: dg.qk_norm_rope(q, k, None, q, k, norm=norm), lambda: dg.qk_norm_rope(q, k, pos, q, k, rope=rope),
+              lambda: dg.paged_attention(b.cache, b.batch, q, q), lambda: dg.paged_append(b.cache, b.batch, k, k)):
+        with pytest.raises(ValueError):
+            f()
+    assert len(old) == 3 and torch.equal(q, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_strides_of_single_rows_and_heads_mean_nothing(dtype):
+    b = Batch(53, dtype, 1, 64, 16, [1], [40])
+    for heads in (6, 1):
+        x = randn(gen(heads), 1, heads, 64, dtype=dtype)
+        odd = (7, 64, 1) if heads > 1 else (7, 5, 1)
+        out, lse = check_attention(b, x, True, dtype)
+        got, q = torch.zeros_like(x), torch.as_strided(x, x.shape, odd)
+        dg.paged_attention(b.cache, b.batch, q, torch.as_strided(got, x.shape, odd))
+        assert torch.equal(got, out)
+
+
 def test_calls_without_rows_do_nothing():
     b = Batch(71, BF, 2, 64, 16, [1], [5])
     q, k = torch.empty(0, 4, 64, dtype=BF, device="cuda"), torch.empty(0, 2, 64, dtype=BF, device="cuda")

@@ -145,6 +145,9 @@ def test_binding_refuses_host_tensors():
         dg.qk_norm_rope(x, None, None, x, None)
     with pytest.raises(ValueError):
         dg.HeadNorm(eps=-1.0)
+    norm = dg.HeadNorm(eps=1e-5)
+    with pytest.raises(AttributeError):   # its address was noted when it was made
+        norm.q_gain = torch.ones(64)
 
 
 def test_structs_match_the_header(tmp_path):
