@@ -240,13 +240,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 //
 // A block is one warp: nothing is shared between warps, and a slot is free as
 // soon as its warp ends, where the block of 8 waited for its last one (26B
-// heads: 16 canvases of 256 tokens 28.7 to 26.6 us, an append of 8192 prompt
+// heads: 32 canvases of 256 tokens 28.7 to 26.6 us, an append of 16384 prompt
 // tokens 61.4 to 55.3, of 64 single tokens 8.2 to 6.7; blocks of 4 and 2 lie
 // between).  What comes from memory without the position (frequencies, gains)
 // is asked for before the sequence is looked up, so the chain of dependent
 // loads is the batch's alone.
 //
-// Many tokens: 4.6 TB/s (101 MB, 22.0 us among others) and 5.3 (268 MB, 51.0 us),
+// Many tokens: 4.6 TB/s (101 MB, 22.1 us among others) and 5.5 (268 MB, 48.4 us),
 // the instructions (1320 a warp) at 16 warps an SM being what is left; few: the
 // launch and two dependent reads (3.3 us).
 template <typename T, int kGroups, bool kInter>
@@ -285,6 +285,24 @@ __global__ void __launch_bounds__(32, 16) k_head_rows(const __grid_constant__ He
 
   const bool all_turn = __all_sync(0xffffffffu, turn_a && turn_b);
 
+  if (kGroups == 4 && b1 - b0 > 2) {
+    // the warp has the whole token: the lines of its later batches start for L2
+    // while the first is worked on (three batches, an append of 16384 prompt
+    // tokens: 51.2 to 48.4 us; two batches, 8192 tokens without values: 22.1
+    // without and 22.6 with it; a batch ahead in registers: a third slower)
+    const int first = min(per_batch, a.n_q ? a.n_q : a.n_k);
+    const int lines = max(1, a.head_dim * (int)sizeof(T) / 128), n = (a.n_q + a.n_k + a.n_v - first) * lines;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      const int head = i / lines, line = i - head * lines;
+      int h = first + head;
+      const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_k ? 1 : 2;
+      h -= kind == 0 ? 0 : kind == 1 ? a.n_q : a.n_q + a.n_k;
+      const HeadRows& in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+      const T* at = (const T*)in.data + (long long)t * in.ts + (long long)h * in.hs + line * (128 / (int)sizeof(T));
+      asm volatile("prefetch.global.L2 [%0];" :: "l"(at));
+    }
+  }
   TokenSpot spot;
   bool have_spot = false;
   float c[N], s[N];
