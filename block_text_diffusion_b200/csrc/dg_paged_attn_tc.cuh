@@ -24,6 +24,13 @@
 // after the last Q K^T) run under the end of the current one.  Each role's
 // code is written once, in a loop over both modes: with the roles unrolled
 // per mode the kernel was 150 KB and spent its time fetching instructions.
+//
+// Measured, with the join: 8 canvases of 256 tokens behind 32768 + 256 keys
+// (8 heads of 128 over 2 key heads) 251 to 285 us, 0.98 to 1.11 PFLOP/s of
+// 1.62: a step of 2 x 128 rows x 128 keys takes 3770 clocks, its MMAs 2560 (the
+// products with Q and K from shared memory run at 80 clocks for 64), its
+// exponentials 2048; what is left is the way from S to P and back.  64 single
+// tokens behind a shared 2048-token prompt 76 us, 4.0 TB/s of keys and values.
 #pragma once
 #include "dg_paged_attn.cuh"
 
