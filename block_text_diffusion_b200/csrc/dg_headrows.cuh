@@ -83,15 +83,18 @@ __device__ __forceinline__ TokenSpot token_spot(const HeadRowsArgs& a, int t) {
     s.live = false;
     return s;
   }
-  const PagedSeq q = paged_seq(b, i);
-  const int own = q.kv - q.nq + (t - q.q0);
-  s.pos = b.prefix_len + own;
-  // own < kv <= max_pages * page_size, so the table entry exists
-  if (own >= 0 && own < q.kv) {
+  const int end = b.cu_q[i + 1], kv = b.kv_lens[i];
+  paged_seq(b, b.cu_q[i], end, kv);   // (reports lengths and offsets out of range)
+  // The token's place by the lengths as they are, not brought into range: one
+  // that lies past the table has no slot, and must not take an earlier token's.
+  const long long own = (long long)kv - end + t;
+  s.pos = (int)(b.prefix_len + own);
+  // (a row past its sequence's end, by offsets that decrease, has none either)
+  if (own >= 0 && own < lmin(kv, (long long)b.max_pages << b.page_shift)) {
     const int page = b.table[(long long)i * b.table_stride + (own >> b.page_shift)];
     if (page >= 0 && page < b.n_pages) {
       s.page = page;
-      s.off = own & ((1 << b.page_shift) - 1);
+      s.off = (int)own & ((1 << b.page_shift) - 1);
     }
   }
   if (s.page < 0) dev_error(b.status, kStatusState);

@@ -45,8 +45,8 @@ DG_HD void paged_error(const PagedBatch& b, int code) {
 #endif
 }
 
-DG_HD PagedSeq paged_seq(const PagedBatch& b, int i) {
-  const int a0 = b.cu_q[i], a1 = b.cu_q[i + 1], kv = b.kv_lens[i];
+// Sequence of the rows a0 .. a1 - 1 and kv tokens, as read.
+DG_HD PagedSeq paged_seq(const PagedBatch& b, int a0, int a1, int kv) {
   PagedSeq s;
   s.q0 = imin(imax(a0, 0), b.n_tokens);
   const int q1 = imin(imax(a1, s.q0), b.n_tokens);
@@ -56,3 +56,4 @@ DG_HD PagedSeq paged_seq(const PagedBatch& b, int i) {
   if (s.q0 != a0 || q1 != a1 || s.kv != kv) paged_error(b, kStatusState);
   return s;
 }
+DG_HD PagedSeq paged_seq(const PagedBatch& b, int i) { return paged_seq(b, b.cu_q[i], b.cu_q[i + 1], b.kv_lens[i]); }

@@ -1,0 +1,66 @@
+"""The paged serving operators' contract where calls go wrong or go far: lengths
+past the table, argument objects whose tensors changed, errors nobody asked
+for, gradients, streams, positions near the ends of int32, kernel variants that
+only many rows reach.  Tolerances as in test_gpu_serving.py unless a test
+derives its own.
+"""
+import copy
+import math
+from decimal import Decimal, getcontext
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import block_text_diffusion_b200 as dg  # noqa: E402
+import test_gpu_serving as base  # noqa: E402
+from test_gpu_serving import BF, F32, Batch, attend, check_attention, freqs, gen, i32, near_turned, randn, turned  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    dg.lib()
+
+
+# -- slots that do not exist -------------------------------------------------------
+
+@pytest.mark.parametrize("hd", [64, 66])   # both kernels
+def test_tokens_past_the_table_or_the_buffers_are_not_stored(hd):
+    """A length past the table, or an offset past the rows, moves no other token:
+    own token j goes to slot j or nowhere."""
+    b = Batch(81, BF, 2, hd, 16, [2, 2, 3, 1, 1], [30, 15, 7, 31, 30])
+    room = b.table.shape[1] * 16
+    table = np.tile(np.arange(b.table.shape[1], dtype=np.int32), (5, 1)) + 3 * np.arange(5, dtype=np.int32)[:, None]
+    pages = 3 * 5
+    k0, v0 = randn(gen(1), pages, 2, 16, hd, dtype=BF), randn(gen(2), pages, 2, 16, hd, dtype=BF)
+    cache = dg.PagedKV(k0.clone(), v0.clone())
+    assert room == 48 and b.table.shape[1] == 3
+    # one token with a slot and one past the table; sound; three tokens of which the buffers hold one ...
+    cu, kv = [0, 2, 4, 7], [room + 1, 17, 10]
+    k, v = randn(gen(3), 5, 2, hd, dtype=BF), randn(gen(4), 5, 2, hd, dtype=BF)
+    q, q_out = randn(gen(5), 5, 4, hd, dtype=BF), torch.zeros(5, 4, hd, dtype=BF, device="cuda")
+    w = freqs(32)[0]
+    status = i32([0])
+    dg.paged_append(cache, dg.PagedBatch(i32(cu), i32(kv), i32(table[:3])), k, v, rope=dg.Rope(w), q=q, q_out=q_out,
+                    status=status)
+    assert int(status) == 5
+    slot = {0: (0, room - 1), 2: (1, 15), 3: (1, 16), 4: (2, 7)}   # row: (sequence, own token)
+    rows = torch.tensor(list(slot), device="cuda")
+    at = torch.tensor([int(table[s, j // 16]) for s, j in slot.values()], device="cuda")
+    off = torch.tensor([j % 16 for _, j in slot.values()], device="cuda")
+    pos = torch.tensor([j for _, j in slot.values()], device="cuda")
+    near_turned(cache.k[at, :, off], *turned(k[rows], pos, w=w))
+    near_turned(q_out[rows], *turned(q[rows], pos, w=w))
+    assert torch.equal(cache.v[at, :, off], v[rows])
+    k0[at, :, off], v0[at, :, off] = cache.k[at, :, off], cache.v[at, :, off]
+    assert torch.equal(k0, cache.k) and torch.equal(v0, cache.v)
+    # ... and lengths at the ends of int32
+    for far in ((1 << 31) - 1, -(1 << 31)):
+        status.zero_()
+        dg.paged_append(cache, dg.PagedBatch(i32([0, 2]), i32([far]), i32(table[:1])), k[:2], v[:2], rope=dg.Rope(w),
+                        status=status)
+        assert int(status) == 5 and torch.equal(k0, cache.k) and torch.equal(v0, cache.v)
