@@ -36,7 +36,7 @@ struct Refused {};   // a Python exception is set
 }
 
 // Interned attribute names.
-#define DG_NAMES(X) X(_at) X(index) X(inv_freq) X(q_gain) X(k_gain) X(k) X(v) X(_words) X(cuda_stream) X(device)
+#define DG_NAMES(X) X(_at) X(index) X(inv_freq) X(q_gain) X(k_gain) X(k) X(v) X(_words) X(_tensors) X(cuda_stream) X(device)
 #define X(n) PyObject* s_##n;
 DG_NAMES(X)
 #undef X
@@ -107,11 +107,12 @@ at::ScalarType model_type(const at::Tensor& t) {
 
 // A tensor whose address an argument object noted when it was made: its memory
 // may have been replaced since (a module moved to another type or device).
-const at::Tensor& held(const Ref& r, const char* name, const void* noted) {
-  const at::Tensor& t = tensor(r.p, name);
+const at::Tensor& held(PyObject* o, const char* name, const void* noted) {
+  const at::Tensor& t = tensor(o, name);
   if (t.data_ptr() != noted) refuse("%s has other memory than when it was given: make the argument object anew", name);
   return t;
 }
+const at::Tensor& held(const Ref& r, const char* name, const void* noted) { return held(r.p, name, noted); }
 
 const dg_rope* rope_of(PyObject* o, int index) {
   if (o == Py_None) return nullptr;
@@ -148,8 +149,10 @@ Cache cache_of(PyObject* o) {
 
 dg_paged_batch batch_of(PyObject* o, const Cache& c, int64_t tokens) {
   Ref w(PyObject_GetAttr(o, s__words));   // index, n_seqs, the addresses, entries of prefix_pages
+  Ref ts(PyObject_GetAttr(o, s__tensors));
   long long v[10];
-  if (!PyTuple_Check(w.p) || PyTuple_GET_SIZE(w.p) != 10) refuse("batch must be a PagedBatch");
+  if (!PyTuple_Check(w.p) || PyTuple_GET_SIZE(w.p) != 10 || !PyTuple_Check(ts.p) || PyTuple_GET_SIZE(ts.p) != 4)
+    refuse("batch must be a PagedBatch");
   for (int i = 0; i < 10; ++i) {
     v[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(w.p, i));
     if (v[i] == -1 && PyErr_Occurred()) throw Refused{};
@@ -166,6 +169,18 @@ dg_paged_batch batch_of(PyObject* o, const Cache& c, int64_t tokens) {
   b.max_pages = (int32_t)v[6];
   b.prefix_pages = (const int32_t*)v[7];
   b.prefix_len = (int32_t)v[8];
+  // every tensor still has the memory and the shape that were noted (a table
+  // that grew in place moved, and the old memory belongs to someone else)
+  auto same = [&](int i, const char* name, const void* noted, at::IntArrayRef shape, bool contiguous) -> const at::Tensor& {
+    return check(held(PyTuple_GET_ITEM(ts.p, i), name, noted), name, at::kInt, shape, c.index, contiguous);
+  };
+  const int64_t offsets = v[1] + 1, seqs = v[1], table[2] = {v[1], v[6]}, prefix = v[9];
+  same(0, "cu_q", b.cu_q, at::IntArrayRef(&offsets, 1), true);
+  same(1, "kv_lens", b.kv_lens, at::IntArrayRef(&seqs, 1), true);
+  const at::Tensor& t = same(2, "page_table", b.page_table, at::IntArrayRef(table, 2), false);
+  if (std::max(t.stride(0), t.size(1)) != b.table_stride || (t.size(1) > 1 && t.stride(1) != 1))
+    refuse("page_table has other strides than when it was given: make the argument object anew");
+  if (b.prefix_len > 0) same(3, "prefix_pages", b.prefix_pages, at::IntArrayRef(&prefix, 1), true);
   if (v[9] * c.c->page_size < b.prefix_len) refuse("prefix_pages has fewer pages than prefix_len needs");
   return b;
 }

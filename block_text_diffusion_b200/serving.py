@@ -7,7 +7,8 @@ asynchronous on `stream` (default: the current stream of the tensors' device),
 allocates nothing but a workspace the caller did not bring, and can be captured
 into a CUDA graph.  Nothing is recorded for a backward pass.  The argument
 objects note the addresses of their tensors, so they cannot be changed after
-they were made; the tensors' contents may.
+they were made; the tensors' contents may.  A tensor that got other memory
+since (resized, moved) is refused.
 
     cache = PagedKV(k_pages, v_pages)                   # [n_pages, Hkv, page, hd]
     batch = PagedBatch(cu_q, kv_lens, page_table)       # device int32
@@ -233,7 +234,8 @@ class PagedBatch(_Fixed):
             _tensor(prefix_pages, "prefix_pages", i32, 1, cu_q.device, contiguous=True)
         self.cu_q, self.kv_lens, self.page_table, self.prefix_pages = cu_q, kv_lens, page_table, prefix_pages
         self.n_seqs, self.prefix_len, self.index = n, int(prefix_len), cu_q.get_device()
-        # what dg_paged_batch needs
+        # what dg_paged_batch needs, and the tensors it comes from (each call checks that they did not move)
+        self._tensors = (cu_q, kv_lens, page_table, prefix_pages)
         self._words = (self.index, n, cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
                        max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
                        prefix_pages.data_ptr() if prefix_len else 0, int(prefix_len),

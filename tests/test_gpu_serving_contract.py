@@ -64,3 +64,38 @@ def test_tokens_past_the_table_or_the_buffers_are_not_stored(hd):
         dg.paged_append(cache, dg.PagedBatch(i32([0, 2]), i32([far]), i32(table[:1])), k[:2], v[:2], rope=dg.Rope(w),
                         status=status)
         assert int(status) == 5 and torch.equal(k0, cache.k) and torch.equal(v0, cache.v)
+
+
+# -- argument objects --------------------------------------------------------------
+
+def test_a_batch_whose_tensors_got_other_memory_is_refused():
+    b = Batch(82, BF, 2, 64, 16, [1, 1], [5, 20], prefix=20)
+    q, k = randn(gen(1), 2, 4, 64, dtype=BF), randn(gen(2), 2, 2, 64, dtype=BF)
+    old = []   # (the noted addresses stay allocated)
+
+    def fresh():
+        return dg.PagedBatch(i32(b.cu), i32(b.kv), i32(b.table), prefix_pages=i32(b.prefix_ids), prefix_len=b.prefix)
+
+    def refused(batch):
+        k0, out = b.k.clone(), q.clone()
+        for f in (lambda: dg.paged_attention(b.cache, batch, q, out), lambda: dg.paged_append(b.cache, batch, k, k)):
+            with pytest.raises(ValueError):
+                f()
+        assert torch.equal(out, q) and torch.equal(b.k, k0)
+
+    for name in ("cu_q", "kv_lens", "page_table", "prefix_pages"):
+        batch = fresh()
+        t = getattr(batch, name)
+        old.append(t.data)
+        t.data = t.clone()
+        refused(batch)
+    # at the same address, with fewer entries or another order
+    for name, change in (("cu_q", lambda t: t.resize_(2)), ("kv_lens", lambda t: t.resize_(1)),
+                         ("page_table", lambda t: t.resize_(2, 1)), ("page_table", lambda t: t.t_()),
+                         ("prefix_pages", lambda t: t.resize_(1))):
+        batch = fresh()
+        change(getattr(batch, name))
+        refused(batch)
+    # and as it was made it is taken
+    check_attention(b, q, True, BF)
+    assert len(old) == 4
