@@ -8,7 +8,8 @@ allocates nothing but a workspace the caller did not bring, and can be captured
 into a CUDA graph.  Nothing is recorded for a backward pass.  The argument
 objects note the addresses of their tensors, so they cannot be changed after
 they were made; the tensors' contents may.  A tensor that got other memory
-since (resized, moved) is refused.
+since (resized, moved) is refused.  A copy notes its own tensors; copy.deepcopy
+copies the tensors too.
 
     cache = PagedKV(k_pages, v_pages)                   # [n_pages, Hkv, page, hd]
     batch = PagedBatch(cu_q, kv_lens, page_table)       # device int32
@@ -109,6 +110,9 @@ class _Fixed:
             raise AttributeError(f"{type(self).__name__}.{name} is fixed: make another {type(self).__name__}")
         self.__dict__[name] = value
 
+    def __reduce__(self):   # a copy notes the addresses of its own tensors
+        return type(self), self._args
+
 
 class Rope(_Fixed):
     """Position rotation: pair j of a head turns by position * inv_freq[j].
@@ -124,6 +128,7 @@ class Rope(_Fixed):
         _need(inv_freq.is_cuda, "inv_freq must be on a GPU")
         self.inv_freq, self.index = inv_freq, inv_freq.get_device()
         self.rot_dim = 2 * inv_freq.numel()
+        self._args = (inv_freq, interleaved, amplitude)
         self._c = _Rope(inv_freq.data_ptr(), self.rot_dim, int(bool(interleaved)), float(amplitude))
         self._at = ctypes.addressof(self._c)
         self._fixed = True
@@ -135,6 +140,7 @@ class HeadNorm(_Fixed):
     def __init__(self, eps=1e-6, q_gain=None, k_gain=None):
         _need(eps >= 0.0, "eps must not be negative")
         self.q_gain, self.k_gain = q_gain, k_gain
+        self._args = (eps, q_gain, k_gain)
         self._c = _HeadNorm(1, float(eps), None if q_gain is None else q_gain.data_ptr(),
                             None if k_gain is None else k_gain.data_ptr())
         self._at = ctypes.addressof(self._c)
@@ -197,6 +203,7 @@ class PagedKV(_Fixed):
         _need(16 <= page <= 256 and page & (page - 1) == 0, "page_size must be a power of two from 16 to 256")
         self.k, self.v, self.dtype, self.device, self.index = k, v, k.dtype, k.device, k.get_device()
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self._args = (k, v)
         self._c = _PagedKV(k.data_ptr(), v.data_ptr(), code, self.n_pages, self.n_kv_heads, page, self.head_dim)
         self._at = ctypes.addressof(self._c)
         self._fixed = True
@@ -236,6 +243,7 @@ class PagedBatch(_Fixed):
         self.n_seqs, self.prefix_len, self.index = n, int(prefix_len), cu_q.get_device()
         # what dg_paged_batch needs, and the tensors it comes from (each call checks that they did not move)
         self._tensors = (cu_q, kv_lens, page_table, prefix_pages)
+        self._args = (cu_q, kv_lens, page_table, prefix_pages, prefix_len)
         self._words = (self.index, n, cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
                        max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
                        prefix_pages.data_ptr() if prefix_len else 0, int(prefix_len),

@@ -99,3 +99,32 @@ def test_a_batch_whose_tensors_got_other_memory_is_refused():
     # and as it was made it is taken
     check_attention(b, q, True, BF)
     assert len(old) == 4
+
+
+def test_copies_of_argument_objects_are_their_own():
+    b = Batch(83, BF, 2, 64, 16, [1, 1], [5, 20], prefix=20)
+    q, k = randn(gen(1), 2, 4, 64, dtype=BF), randn(gen(2), 2, 2, 64, dtype=BF)
+    w, _ = freqs(64)
+    gain, pos = 1 + randn(gen(3), 64, dtype=BF, std=0.2), i32([3, 9])
+    first = check_attention(b, q, True, BF)
+    rope, norm = dg.Rope(w, interleaved=True, amplitude=1.5), dg.HeadNorm(1e-5, gain)
+    want = torch.empty_like(q)
+    dg.qk_norm_rope(q, None, pos, want, None, rope=rope, norm=norm)
+    for how in (copy.copy, copy.deepcopy):
+        batch, cache, rope2, norm2 = how(b.batch), how(b.cache), how(rope), how(norm)
+        out = torch.empty_like(q)
+        dg.paged_attention(cache, batch, q, out)
+        assert torch.equal(out, first[0])
+        dg.qk_norm_rope(q, None, pos, out, None, rope=rope2, norm=norm2)
+        assert torch.equal(out, want)
+        assert (batch.kv_lens.data_ptr() == b.batch.kv_lens.data_ptr()) == (how is copy.copy)
+    # the deep copy reads its own lengths and writes its own pages
+    batch.kv_lens.copy_(i32([3, 21]))
+    b.kv = [3, 21]
+    out = torch.empty_like(q)
+    dg.paged_attention(b.cache, batch, q, out)
+    saved, b.batch = b.batch, batch
+    assert torch.equal(check_attention(b, q, True, BF)[0], out) and not torch.equal(out, first[0])
+    k0 = b.k.clone()
+    dg.paged_append(cache, saved, k, k)
+    assert torch.equal(b.k, k0) and not torch.equal(cache.k, k0)
