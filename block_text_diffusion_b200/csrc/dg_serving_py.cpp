@@ -62,7 +62,9 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
-const char* type_name(at::ScalarType t) { return t == at::kBFloat16 ? "bfloat16" : t == at::kFloat ? "float32" : "int32"; }
+const char* type_name(at::ScalarType t) {
+  return t == at::kBFloat16 ? "bfloat16" : t == at::kFloat ? "float32" : t == at::kDouble ? "float64" : "int32";
+}
 
 // A tensor of a type and shape on a device.
 const at::Tensor& check(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, int index,
@@ -107,6 +109,7 @@ at::ScalarType model_type(const at::Tensor& t) {
 
 // A tensor whose address an argument object noted when it was made: its memory
 // may have been replaced since (a module moved to another type or device).
+// What else was noted (shape, type, order) is checked beside it.
 const at::Tensor& held(PyObject* o, const char* name, const void* noted) {
   const at::Tensor& t = tensor(o, name);
   if (t.data_ptr() != noted) refuse("%s has other memory than when it was given: make the argument object anew", name);
@@ -118,7 +121,8 @@ const dg_rope* rope_of(PyObject* o, int index) {
   if (o == Py_None) return nullptr;
   Ref freq(PyObject_GetAttr(o, s_inv_freq));   // (only a Rope has it)
   const dg_rope* r = reinterpret_cast<const dg_rope*>(attr_int(o, s__at));
-  if (held(freq, "inv_freq", r->inv_freq).get_device() != index) refuse("inv_freq must be on cuda:%d", index);
+  const int64_t pairs = r->rot_dim / 2;
+  check(held(freq, "inv_freq", r->inv_freq), "inv_freq", at::kDouble, at::IntArrayRef(&pairs, 1), index, true);
   return r;
 }
 
@@ -140,10 +144,11 @@ Cache cache_of(PyObject* o) {
   Cache r;
   Ref k(PyObject_GetAttr(o, s_k)), v(PyObject_GetAttr(o, s_v));   // (only a PagedKV has them)
   r.c = reinterpret_cast<const dg_paged_kv*>(attr_int(o, s__at));
-  held(k, "the cache's k", r.c->k);
-  held(v, "the cache's v", r.c->v);
   r.index = (int)attr_int(o, s_index);
   r.type = r.c->dtype == DG_BF16 ? at::kBFloat16 : at::kFloat;
+  const int64_t shape[4] = {r.c->n_pages, r.c->n_kv_heads, r.c->page_size, r.c->head_dim};
+  check(held(k, "the cache's k", r.c->k), "the cache's k", r.type, at::IntArrayRef(shape, 4), r.index, true);
+  check(held(v, "the cache's v", r.c->v), "the cache's v", r.type, at::IntArrayRef(shape, 4), r.index, true);
   return r;
 }
 

@@ -7,8 +7,8 @@ asynchronous on `stream` (default: the current stream of the tensors' device),
 allocates nothing but a workspace the caller did not bring, and can be captured
 into a CUDA graph.  Nothing is recorded for a backward pass.  The argument
 objects note the addresses of their tensors, so they cannot be changed after
-they were made; the tensors' contents may.  A tensor that got other memory
-since (resized, moved) is refused.  A copy notes its own tensors; copy.deepcopy
+they were made; the tensors' contents may.  A tensor that got other memory or
+another shape since (resized, moved, transposed in place) is refused.  A copy notes its own tensors; copy.deepcopy
 copies the tensors too.
 
     cache = PagedKV(k_pages, v_pages)                   # [n_pages, Hkv, page, hd]

@@ -128,3 +128,22 @@ def test_copies_of_argument_objects_are_their_own():
     k0 = b.k.clone()
     dg.paged_append(cache, saved, k, k)
     assert torch.equal(b.k, k0) and not torch.equal(cache.k, k0)
+
+
+def test_tensors_reshaped_in_place_are_refused():
+    """The same address with another shape, order or type is not what was noted."""
+    b = Batch(84, BF, 16, 64, 16, [1, 1], [5, 20])   # (16 heads, 16 slots: a transposed cache has its old shape)
+    q, k = randn(gen(1), 2, 16, 64, dtype=BF), randn(gen(2), 2, 16, 64, dtype=BF)
+    pos, out = i32([0, 1]), torch.zeros(2, 16, 64, dtype=BF, device="cuda")
+    for change in (lambda c: c.k.transpose_(1, 2), lambda c: c.v.transpose_(1, 2), lambda c: c.k.resize_(1, 16, 16, 64),
+                   lambda c: c.v.squeeze_().resize_(2, 16, 16, 64)):
+        cache = dg.PagedKV(b.k.clone(), b.v.clone())
+        change(cache)
+        for f in (lambda: dg.paged_attention(cache, b.batch, q, out), lambda: dg.paged_append(cache, b.batch, k, k)):
+            with pytest.raises(ValueError):
+                f()
+    rope = dg.Rope(freqs(64)[0])
+    rope.inv_freq.resize_(16)
+    with pytest.raises(ValueError):
+        dg.qk_norm_rope(q, None, pos, out, None, rope=rope)
+    assert torch.all(out == 0)
