@@ -14,7 +14,7 @@ import os
 from . import inputs  # noqa: F401  (seeded synthetic inputs)
 from . import serving
 from .serving import (HeadNorm, PagedBatch, PagedKV, Rope, paged_append, paged_attention,  # noqa: F401
-                      paged_attention_workspace, qk_norm_rope, rope_frequencies)
+                      paged_attention_workspace, qk_norm_rope, rope_frequencies, serving_status)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")

@@ -97,7 +97,7 @@ __device__ __forceinline__ TokenSpot token_spot(const HeadRowsArgs& a, int t) {
       s.off = (int)own & ((1 << b.page_shift) - 1);
     }
   }
-  if (s.page < 0) dev_error(b.status, kStatusState);
+  if (s.page < 0) paged_error(b, kStatusState);
   return s;
 }
 

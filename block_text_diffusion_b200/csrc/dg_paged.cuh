@@ -8,6 +8,11 @@
 // The caller's arrays are device memory the host never looks at, so every
 // value read from them is brought into range before it is used as an index
 // and reported through the status word when it was out of range.
+
+// The word of calls that were given none: one on each device, zero until an
+// error, read and cleared by dg_serving_status.
+__device__ int g_serving_status;
+
 struct PagedBatch {
   int n_seqs, n_tokens;
   const int* cu_q;
@@ -18,7 +23,7 @@ struct PagedBatch {
   const int* prefix_pages;
   int prefix_len;
   int n_pages, page_shift;   // page size = 1 << page_shift
-  int* status;
+  int* status;               // null: the device's own word
 };
 
 struct PagedSeq {
@@ -39,7 +44,7 @@ DG_HD long long lmax(long long a, long long b) { return a > b ? a : b; }
 
 DG_HD void paged_error(const PagedBatch& b, int code) {
 #ifdef __CUDA_ARCH__
-  dev_error(b.status, code);
+  dev_error(b.status ? b.status : &g_serving_status, code);
 #else
   if (b.status && *b.status == 0) *b.status = code;
 #endif

@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(256, 1) k_paged_attn_f32(const __grid_constant
           const int page = f.page_list[key >> a.b.page_shift];
           ok = page >= 0 && page < a.b.n_pages;
           if (ok) off = ((((long long)page * a.n_kv_heads + f.kvh) << a.b.page_shift) + (key & page_mask)) * kHd + c;
-          else dev_error(a.b.status, kStatusState);
+          else paged_error(a.b, kStatusState);
         }
         cp_async_16z(sK + r * kLd + c, (const float*)a.k_pages + off, ok);
         cp_async_16z(sV + r * kHd + c, (const float*)a.v_pages + off, ok);

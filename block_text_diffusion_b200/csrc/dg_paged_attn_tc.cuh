@@ -126,7 +126,7 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 __device__ __noinline__ bool pa_wait_slow(uint64_t* bar, uint32_t parity, int* err) {
   for (int i = 0; i < 64; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, err, kStatusTimeout);
+  return mbar_wait(bar, parity, err ? err : &g_serving_status, kStatusTimeout);
 }
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, int* err) {
   bool ok = mbar_try_wait(bar, parity);
@@ -249,7 +249,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           if (pg0 + lane < f.pages) {
             id = f.page_list[pg0 + lane];
             if (id < 0 || id >= a.b.n_pages) {
-              dev_error(err, kStatusState);
+              paged_error(a.b, kStatusState);
               id = a.b.n_pages;   // past the tensor's end: reads as zeros
             }
           }

@@ -1,5 +1,6 @@
 // Serving operators over a paged key/value cache (include/dg.h): argument
-// checks, launch choices and launches.  Nothing is kept between calls.
+// checks, launch choices and launches.  Nothing is kept between calls but an
+// error that a call without a status word met.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -365,6 +366,19 @@ extern "C" dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged
   a.slot_o = (float*)(ws + sp.slot_o);
   return hd == 64 ? run_paged_attention<64>(cache, a, (cudaStream_t)stream)
                   : run_paged_attention<128>(cache, a, (cudaStream_t)stream);
+}
+
+extern "C" dg_status dg_serving_status(void* stream) {
+  const cudaStream_t s = (cudaStream_t)stream;
+  int code = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&code, g_serving_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && code) {
+    const int none = 0;
+    e = cudaMemcpyToSymbolAsync(g_serving_status, &none, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
+  return e == cudaSuccess ? (dg_status)code : done(e);
 }
 
 extern "C" dg_status dg_test_paged_walk(const dg_paged_kv* cache, const dg_paged_batch* batch, int32_t n_heads,

@@ -8,8 +8,9 @@ allocates nothing but a workspace the caller did not bring, and can be captured
 into a CUDA graph.  Nothing is recorded for a backward pass.  The argument
 objects note the addresses of their tensors, so they cannot be changed after
 they were made; the tensors' contents may.  A tensor that got other memory or
-another shape since (resized, moved, transposed in place) is refused.  A copy notes its own tensors; copy.deepcopy
-copies the tensors too.
+another shape since (resized, moved, transposed in place) is refused.  A copy
+notes its own tensors; copy.deepcopy copies the tensors too.  Errors that only
+the device finds go to the call's status word, or to serving_status().
 
     cache = PagedKV(k_pages, v_pages)                   # [n_pages, Hkv, page, hd]
     batch = PagedBatch(cu_q, kv_lens, page_table)       # device int32
@@ -56,6 +57,7 @@ def signatures():
         "dg_paged_append": ([_P, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _P], _I32),
         "dg_paged_attention_workspace": ([_I32, _I32, _I32, _I32], ctypes.c_size_t),
         "dg_paged_attention": ([_P, _P, _I32, _P, _F, _I32, _P, _P, _P, ctypes.c_size_t, _P, _P], _I32),
+        "dg_serving_status": ([_P], _I32),
         "dg_test_paged_walk": ([_P, _P, _I32, _I32, _I32, _P, _P, _I32, _P], _I32),
     }
 
@@ -265,7 +267,7 @@ def paged_append(cache, batch, k, v, rope=None, norm=None, q=None, q_out=None, s
     queries, normalised and rotated, into q_out (which may be q).
 
     status: int32 [1] device tensor, zero before; becomes 5 (DG_ERR_STATE) if a
-    token had no valid slot (it is not stored)."""
+    token had no valid slot (it is not stored).  None: see serving_status."""
     _native().paged_append(cache, batch, k, v, rope, norm, q, q_out, status, stream)
 
 
@@ -288,7 +290,8 @@ def paged_attention(cache, batch, q, out, scale=None, causal=True, lse=None, wor
     key gets zeros and -inf.  workspace: uint8 tensor of at least
     paged_attention_workspace(...) bytes (None: allocated for the call); two
     calls that may overlap need two.  status: int32 [1], zero before; becomes 5
-    (DG_ERR_STATE) if a page id or length was out of range."""
+    (DG_ERR_STATE) if a page id or length was out of range, 4 (DG_ERR_TIMEOUT) if
+    a wait ran out.  None: see serving_status."""
     call = _native().paged_attention
     if workspace is None:
         import torch
@@ -303,3 +306,15 @@ def paged_attention(cache, batch, q, out, scale=None, causal=True, lse=None, wor
         with torch.cuda.stream(torch.cuda.current_stream(cache.device) if stream is None else stream):
             workspace = torch.empty(n, dtype=torch.uint8, device=cache.device)
     call(cache, batch, q, out, scale, causal, lse, workspace, status, stream)
+
+
+def serving_status(stream=None):
+    """Waits for `stream` (default: the current one) and raises DGError for the
+    first error that calls without a status tensor met on its device since this
+    was last asked (a token without a slot, a page id or length out of range, a
+    wait that ran out).  The outputs of such a call are not to be used."""
+    import torch
+
+    from . import _check, _stream, lib
+    with torch.cuda.device(torch.cuda.current_device() if stream is None else stream.device):
+        _check(lib().dg_serving_status(_stream(stream)), "device status")

@@ -216,14 +216,15 @@ dg_status dg_gemm_splitk_noalloc(const void* A, const void* B, float* out, int32
  * by side without one padded cache per canvas.
  *
  * All three are asynchronous on `stream`, allocate nothing, keep nothing
- * between calls and may be captured into a CUDA graph (lengths, page tables
- * and positions are read on the device at each replay).  Calls that overlap
- * on the GPU need separate outputs and workspaces, nothing else.  Argument
- * errors are returned at once with nothing enqueued.  Errors found on the
- * device (a page id or a length out of range, a wait that ran out) are
+ * between calls (but an error) and may be captured into a CUDA graph (lengths,
+ * page tables and positions are read on the device at each replay).  Calls that
+ * overlap on the GPU need separate outputs and workspaces, nothing else.
+ * Argument errors are returned at once with nothing enqueued.  Errors found on
+ * the device (a page id or a length out of range, a wait that ran out) are
  * written, first one wins, into `status_word`, a device int32 that the caller
- * sets to 0 (NULL: not reported): DG_ERR_STATE or DG_ERR_TIMEOUT.  No call
- * reads or writes outside the buffers it was given, whatever these arrays hold.
+ * sets to 0 (NULL: latched in a word of the device's own, returned by
+ * dg_serving_status): DG_ERR_STATE or DG_ERR_TIMEOUT.  No call reads or writes
+ * outside the buffers it was given, whatever these arrays hold.
  *
  * Strides count elements.  The components of a head are always contiguous.
  * ------------------------------------------------------------------------- */
@@ -320,6 +321,11 @@ size_t dg_paged_attention_workspace(int32_t n_tokens, int32_t n_heads, int32_t h
 dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged_batch* batch, int32_t n_heads,
                              const dg_heads* q, float scale, int32_t causal, const dg_heads* out, float* lse,
                              void* workspace, size_t workspace_bytes, int32_t* status_word, void* stream);
+
+/* Wait for `stream` and return the first error that serving calls without a
+ * status word met on the current device (DG_ERR_TIMEOUT, DG_ERR_STATE) or DG_OK;
+ * clears the latch.  Not during a capture. */
+dg_status dg_serving_status(void* stream);
 
 #ifdef __cplusplus
 }

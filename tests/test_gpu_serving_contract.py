@@ -147,3 +147,41 @@ def test_tensors_reshaped_in_place_are_refused():
     with pytest.raises(ValueError):
         dg.qk_norm_rope(q, None, pos, out, None, rope=rope)
     assert torch.all(out == 0)
+
+
+# -- errors nobody gave a word for -------------------------------------------------
+
+def test_errors_without_a_status_word_are_kept_for_serving_status():
+    dg.serving_status()   # whatever earlier calls left
+    b = Batch(85, BF, 2, 64, 16, [1, 1], [40, 40], prefix=20)
+    q, k = randn(gen(1), 2, 4, 64, dtype=BF), randn(gen(2), 2, 2, 64, dtype=BF)
+    out = torch.empty_like(q)
+    table = b.table.copy()
+    table[0, 2] = b.n_pages
+    bad = dg.PagedBatch(i32(b.cu), i32(b.kv), i32(table))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        dg.paged_attention(b.cache, bad, q, out)
+    f32 = Batch(86, F32, 2, 64, 16, [1], [40])
+    x = randn(gen(3), 1, 2, 64)
+    for call in (lambda: dg.paged_append(b.cache, bad, k, k), lambda: dg.paged_attention(b.cache, bad, q, out),
+                 lambda: dg.paged_attention(f32.cache, dg.PagedBatch(i32([0, 1]), i32([41]), i32([[0, -1, 0]])), x, x),
+                 graph.replay):
+        call()
+        torch.cuda.synchronize()
+        with pytest.raises(dg.DGError) as e:
+            dg.serving_status()
+        assert e.value.code == 5
+        dg.serving_status()   # asked once, gone
+    # a call with a word of its own reports there, a sound one nowhere
+    word = i32([0])
+    dg.paged_append(b.cache, bad, k, k, status=word)
+    dg.paged_attention(b.cache, b.batch, q, out)
+    assert int(word) == 5
+    dg.serving_status()
+    # on a stream of the caller's
+    with torch.cuda.stream(side):
+        dg.paged_append(b.cache, bad, k, k)
+    with pytest.raises(dg.DGError):
+        dg.serving_status(stream=side)
+    del graph
