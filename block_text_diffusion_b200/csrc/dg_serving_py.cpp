@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -66,6 +67,13 @@ const char* type_name(at::ScalarType t) {
   return t == at::kBFloat16 ? "bfloat16" : t == at::kFloat ? "float32" : t == at::kDouble ? "float64" : "int32";
 }
 
+// Nothing is recorded for a backward pass, so a tensor that wants a gradient is
+// an error while gradients are recorded, not one silently dropped.
+void no_gradient(const at::Tensor& t, const char* name) {
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    refuse("%s requires a gradient, which this call does not record: call it under torch.no_grad()", name);
+}
+
 // A tensor of a type and shape on a device.
 const at::Tensor& check(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, int index,
                         bool contiguous) {
@@ -76,6 +84,7 @@ const at::Tensor& check(const at::Tensor& t, const char* name, at::ScalarType ty
     refuse("%s must be a %s%s tensor of shape %R on cuda:%d", name, contiguous ? "contiguous " : "", type_name(type),
            want.p, index);
   }
+  no_gradient(t, name);
   return t;
 }
 

@@ -5,7 +5,8 @@ short); the work is in libdg.so.  Tensors may be views with any token and head
 stride as long as the components of a head are contiguous.  Every call is
 asynchronous on `stream` (default: the current stream of the tensors' device),
 allocates nothing but a workspace the caller did not bring, and can be captured
-into a CUDA graph.  Nothing is recorded for a backward pass.  The argument
+into a CUDA graph.  Nothing is recorded for a backward pass: tensors that
+require a gradient are refused unless gradients are off.  The argument
 objects note the addresses of their tensors, so they cannot be changed after
 they were made; the tensors' contents may.  A tensor that got other memory or
 another shape since (resized, moved, transposed in place) is refused.  A copy

@@ -185,3 +185,36 @@ def test_errors_without_a_status_word_are_kept_for_serving_status():
     with pytest.raises(dg.DGError):
         dg.serving_status(stream=side)
     del graph
+
+
+# -- autograd ----------------------------------------------------------------------
+
+def test_tensors_that_want_a_gradient_are_refused():
+    b = Batch(87, BF, 2, 64, 16, [1, 1], [5, 20])
+    q, k = randn(gen(1), 2, 4, 64, dtype=BF), randn(gen(2), 2, 2, 64, dtype=BF)
+    out, k_out, lse, pos = torch.zeros_like(q), torch.zeros_like(k), torch.zeros(2, 4, device="cuda"), i32([0, 1])
+    w, gain = freqs(64)[0], torch.ones(64, dtype=BF, device="cuda")
+    rope, norm = dg.Rope(w), dg.HeadNorm(1e-6, gain, gain)
+    calls = {
+        "rope": (lambda: dg.qk_norm_rope(q, k, pos, out, k_out, rope=rope, norm=norm), (q, k, out, k_out, w, gain)),
+        "append": (lambda: dg.paged_append(b.cache, b.batch, k, k_out, rope=rope, norm=norm, q=q, q_out=out),
+                   (q, k, k_out, out, b.k, b.v, w, gain)),
+        "attention": (lambda: dg.paged_attention(b.cache, b.batch, q, out, lse=lse), (q, out, lse, b.k, b.v)),
+    }
+    for name, (call, tensors) in calls.items():
+        for i, t in enumerate(tensors):
+            t.requires_grad_(True)
+            with pytest.raises(ValueError, match="gradient"):
+                call()
+                pytest.fail(f"{name}: tensor {i} was taken")
+            with torch.no_grad():
+                call()
+            with torch.inference_mode():
+                call()
+            t.requires_grad_(False)
+        call()
+    # inference tensors are taken too
+    with torch.inference_mode():
+        x = q.clone()
+        dg.qk_norm_rope(x, None, None, x, None, norm=norm)
+    dg.qk_norm_rope(x, None, None, x, None, norm=norm)
