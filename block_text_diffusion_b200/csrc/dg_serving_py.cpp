@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
+#include <initializer_list>
 
 #include "../../include/dg.h"
 
@@ -221,8 +222,20 @@ struct On {
   }
 };
 
-PyObject* finish(dg_status st, const char* name) {
-  if (st == DG_OK) Py_RETURN_NONE;
+// A tensor the call writes: what autograd saved of it is no longer what it was.
+// (Inference tensors keep no count.)
+void wrote(PyObject* o) {
+  if (o == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+// Ends a call whose outputs are `out`.
+PyObject* finish(dg_status st, const char* name, std::initializer_list<PyObject*> out) {
+  if (st == DG_OK) {
+    for (PyObject* o : out) wrote(o);
+    Py_RETURN_NONE;
+  }
   Ref args(Py_BuildValue("(is)", (int)st, name));
   Ref e(PyObject_CallObject(g.error, args.p));
   PyErr_SetObject(g.error, e.p);
@@ -275,7 +288,7 @@ PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     On on(index, a[7]);
     return finish(g.norm_rope(type == at::kBFloat16 ? DG_BF16 : DG_FP32, (int32_t)tokens, (int32_t)hq, (int32_t)hk,
                               (int32_t)dim, &qr, &qo, &kr, &ko, positions, rope, norm, on.stream),
-                  "dg_qk_norm_rope");
+                  "dg_qk_norm_rope", {a[3], a[4]});
   });
 }
 
@@ -303,7 +316,9 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const dg_paged_batch b = batch_of(a[1], c, tokens);
     int32_t* status = status_of(a[8], c.index);
     On on(c.index, a[9]);
-    return finish(g.append(c.c, &b, &kr, &vr, rope, norm, (int32_t)hq, &qr, &qo, status, on.stream), "dg_paged_append");
+    Ref k_pages(PyObject_GetAttr(a[0], s_k)), v_pages(PyObject_GetAttr(a[0], s_v));
+    return finish(g.append(c.c, &b, &kr, &vr, rope, norm, (int32_t)hq, &qr, &qo, status, on.stream), "dg_paged_append",
+                  {k_pages.p, v_pages.p, a[7], a[8]});
   });
 }
 
@@ -343,7 +358,7 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     On on(c.index, a[9]);
     return finish(g.attention(c.c, &b, (int32_t)hq, &qr, (float)scale, causal, &o, lse, ws.data_ptr(),
                               (size_t)ws.numel(), status, on.stream),
-                  "dg_paged_attention");
+                  "dg_paged_attention", {a[3], a[6], a[7], a[8]});
   });
 }
 

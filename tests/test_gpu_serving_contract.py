@@ -218,3 +218,26 @@ def test_tensors_that_want_a_gradient_are_refused():
         x = q.clone()
         dg.qk_norm_rope(x, None, None, x, None, norm=norm)
     dg.qk_norm_rope(x, None, None, x, None, norm=norm)
+
+
+def test_written_tensors_are_seen_by_autograd():
+    """What another operator saved for its backward pass and a call then wrote over
+    ends that pass with an error, as any write in place does."""
+    b = Batch(88, F32, 2, 64, 16, [1, 1], [5, 20])
+    q, k = randn(gen(1), 2, 4, 64), randn(gen(2), 2, 2, 64)
+    out, k_out, lse = torch.zeros_like(q), torch.zeros_like(k), torch.zeros(2, 4, device="cuda")
+    norm = dg.HeadNorm(1e-6)
+    p = torch.ones((), device="cuda", requires_grad=True)
+    for call, written, read in (
+            (lambda: dg.qk_norm_rope(q, k, None, out, k_out, norm=norm), (out, k_out), (q, k)),
+            (lambda: dg.paged_append(b.cache, b.batch, k, k_out, q=q, q_out=out), (b.k, b.v, out), (q, k, k_out)),
+            (lambda: dg.paged_attention(b.cache, b.batch, q, out, lse=lse), (out, lse), (q, b.k, b.v))):
+        for t in written:
+            y = (p * t).sum()
+            call()
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.backward()
+        for t in read:
+            y = (p * t).sum()
+            call()
+            y.backward()
