@@ -6,6 +6,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -38,7 +39,9 @@ struct Refused {};   // a Python exception is set
 }
 
 // Interned attribute names.
-#define DG_NAMES(X) X(_at) X(index) X(inv_freq) X(q_gain) X(k_gain) X(k) X(v) X(_words) X(_tensors) X(cuda_stream) X(device)
+#define DG_NAMES(X)                                                                                                 \
+  X(_at) X(index) X(inv_freq) X(q_gain) X(k_gain) X(k) X(v) X(cu_q) X(kv_lens) X(page_table) X(prefix_pages) X(_words) \
+  X(_tensors) X(cuda_stream) X(device)
 #define X(n) PyObject* s_##n;
 DG_NAMES(X)
 #undef X
@@ -209,16 +212,34 @@ int32_t* status_of(PyObject* o, int index) {
 // The tensors' device is current for the length of a call.
 struct On {
   c10::cuda::OptionalCUDAGuard guard;
+  const int index;
   void* stream;
-  On(int index, PyObject* s) {
+  bool other = false;   // a stream of the caller's, not the current one
+  On(int index_, PyObject* s) : index(index_) {
+    stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
     if (s != Py_None) {
       Ref dev(PyObject_GetAttr(s, s_device));
       if (attr_int(dev.p, s_index) != index) refuse("stream must be one of cuda:%d", index);
-      stream = (void*)attr_int(s, s_cuda_stream);
-    } else {
-      stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
+      void* const own = (void*)attr_int(s, s_cuda_stream);
+      other = own != stream;
+      stream = own;
     }
     if (c10::cuda::current_device() != index) guard.set_index((c10::DeviceIndex)index);
+  }
+  // Tensors were mostly made on the current stream; freed while a call on
+  // another still uses them, their memory must not be given out yet.
+  void uses(PyObject* o) const {
+    if (other && THPVariable_Check(o))
+      c10::cuda::CUDACachingAllocator::recordStream(
+          THPVariable_Unpack(o).storage().data_ptr(),
+          c10::cuda::getStreamFromExternal((cudaStream_t)stream, (c10::DeviceIndex)index));
+  }
+  void uses(PyObject* o, std::initializer_list<PyObject*> names) const {   // an argument object's tensors
+    if (!other || o == Py_None) return;
+    for (PyObject* n : names) {
+      Ref t(PyObject_GetAttr(o, n));
+      uses(t.p);
+    }
   }
 };
 
@@ -286,6 +307,9 @@ PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (rope && a[2] == Py_None) refuse("rope needs positions");
     const dg_head_norm* norm = norm_of(a[6], type, dim, index);
     On on(index, a[7]);
+    for (int i : {0, 1, 2, 3, 4}) on.uses(a[i]);
+    on.uses(a[5], {s_inv_freq});
+    on.uses(a[6], {s_q_gain, s_k_gain});
     return finish(g.norm_rope(type == at::kBFloat16 ? DG_BF16 : DG_FP32, (int32_t)tokens, (int32_t)hq, (int32_t)hk,
                               (int32_t)dim, &qr, &qo, &kr, &ko, positions, rope, norm, on.stream),
                   "dg_qk_norm_rope", {a[3], a[4]});
@@ -316,6 +340,11 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const dg_paged_batch b = batch_of(a[1], c, tokens);
     int32_t* status = status_of(a[8], c.index);
     On on(c.index, a[9]);
+    for (int i : {2, 3, 6, 7, 8}) on.uses(a[i]);
+    on.uses(a[0], {s_k, s_v});
+    on.uses(a[1], {s_cu_q, s_kv_lens, s_page_table, s_prefix_pages});
+    on.uses(a[4], {s_inv_freq});
+    on.uses(a[5], {s_q_gain, s_k_gain});
     Ref k_pages(PyObject_GetAttr(a[0], s_k)), v_pages(PyObject_GetAttr(a[0], s_v));
     return finish(g.append(c.c, &b, &kr, &vr, rope, norm, (int32_t)hq, &qr, &qo, status, on.stream), "dg_paged_append",
                   {k_pages.p, v_pages.p, a[7], a[8]});
@@ -356,6 +385,9 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (ws.scalar_type() != at::kByte || ws.dim() != 1 || !ws.is_cuda() || ws.get_device() != c.index || !ws.is_contiguous())
       refuse("workspace must be a contiguous 1-D uint8 tensor on cuda:%d", c.index);
     On on(c.index, a[9]);
+    for (int i : {2, 3, 6, 7, 8}) on.uses(a[i]);
+    on.uses(a[0], {s_k, s_v});
+    on.uses(a[1], {s_cu_q, s_kv_lens, s_page_table, s_prefix_pages});
     return finish(g.attention(c.c, &b, (int32_t)hq, &qr, (float)scale, causal, &o, lse, ws.data_ptr(),
                               (size_t)ws.numel(), status, on.stream),
                   "dg_paged_attention", {a[3], a[6], a[7], a[8]});

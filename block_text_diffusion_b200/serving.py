@@ -4,6 +4,7 @@ Argument checks and marshalling (in C++, csrc/dg_serving_py.cpp: the calls are
 short); the work is in libdg.so.  Tensors may be views with any token and head
 stride as long as the components of a head are contiguous.  Every call is
 asynchronous on `stream` (default: the current stream of the tensors' device),
+keeps the memory of what it was passed until it has run there,
 allocates nothing but a workspace the caller did not bring, and can be captured
 into a CUDA graph.  Nothing is recorded for a backward pass: tensors that
 require a gradient are refused unless gradients are off.  The argument

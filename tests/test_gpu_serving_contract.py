@@ -241,3 +241,41 @@ def test_written_tensors_are_seen_by_autograd():
             y = (p * t).sum()
             call()
             y.backward()
+
+
+# -- streams -----------------------------------------------------------------------
+
+def test_tensors_of_a_call_on_another_stream_outlive_it():
+    """A caller may drop what it passed as soon as the call returns, on whatever
+    stream the call runs."""
+    t, h, hd = 3001, 16, 128
+    side, norm = torch.cuda.Stream(), dg.HeadNorm(1e-6)
+    out, want = torch.zeros(t, h, hd, dtype=BF, device="cuda"), torch.empty(t, h, hd, dtype=BF, device="cuda")
+    q = randn(gen(1), t, h, hd, dtype=BF)
+    dg.qk_norm_rope(q, None, None, want, None, norm=norm)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)   # a tenth of a second
+    dg.qk_norm_rope(q, None, None, out, None, norm=norm, stream=side)
+    del q
+    others = [torch.full((t, h, hd), 5.0, dtype=BF, device="cuda") for _ in range(3)]   # would take its memory
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(others) == 3
+
+    # the same of an attention call's query, page table and workspace
+    b = Batch(89, BF, 2, 128, 64, [300] * 8, [100] * 8)
+    q = randn(gen(2), b.rows, 16, 128, dtype=BF)
+    want = torch.empty_like(q)
+    dg.paged_attention(b.cache, b.batch, q, want)
+    out = torch.zeros_like(q)
+    ws = torch.empty(dg.paged_attention_workspace(b.rows, 16, 128), dtype=torch.uint8, device="cuda")
+    batch = dg.PagedBatch(i32(b.cu), i32(b.kv), i32(b.table))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    dg.paged_attention(b.cache, batch, q, out, workspace=ws, stream=side)
+    shapes = [(q.shape, q.dtype), (ws.shape, ws.dtype), (batch.page_table.shape, torch.int32), (batch.kv_lens.shape, torch.int32)]
+    del q, ws, batch
+    others = [torch.zeros(s, dtype=d, device="cuda") for s, d in shapes for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(others) == 12
