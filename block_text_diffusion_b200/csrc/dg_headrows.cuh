@@ -6,10 +6,12 @@
 //   t = position * inv_freq[j]                       (the first rot_dim components)
 //
 // Angles: position * inv_freq reaches 1e5 radians and more in a long context,
-// where binary32 has lost the phase.  The product is formed in fp64 in units
-// of a turn, its whole turns are dropped there, and sincospi takes the
-// remainder in [-1/2, 1/2] turns in fp32: the sine and cosine are good to
-// fp32 rounding at every position.
+// where binary32 has lost the phase, and at the ends of int32 a product rounded
+// to fp64 is off by 5e-7.  So the product is formed in units of a turn as a sum
+// of two fp64 values (the rounding of 1 / (2 pi), of the frequency and of the
+// product are kept), its whole turns are dropped, and sincospi takes the
+// remainder in [-1/2, 1/2] turns in fp32: the sine and cosine are good to fp32
+// rounding (4 units of 2^-24) at every position.
 //
 // Everything is read once and written once, in fp32 between; one rounding.
 #pragma once
@@ -102,8 +104,10 @@ __device__ __forceinline__ TokenSpot token_spot(const HeadRowsArgs& a, int t) {
 }
 
 __device__ __forceinline__ void turn_sincos(int pos, double inv_freq, float amplitude, float& c, float& s) {
-  const double turns = (double)pos * (inv_freq * 0.15915494309189533577);   // 1 / (2 pi)
-  const float r = (float)(turns - rint(turns));
+  constexpr double kTurn = 0.15915494309189533577, kTurnLo = -9.839338337591243e-18;   // 1 / (2 pi), and what that leaves
+  const double f = inv_freq * kTurn, f_lo = fma(inv_freq, kTurn, -f) + inv_freq * kTurnLo;
+  const double turns = pos * f, turns_lo = fma((double)pos, f, -turns) + pos * f_lo;
+  const float r = (float)((turns - rint(turns)) + turns_lo);
   sincospif(2.0f * r, &s, &c);
   c *= amplitude;
   s *= amplitude;

@@ -279,3 +279,36 @@ def test_tensors_of_a_call_on_another_stream_outlive_it():
     others = [torch.zeros(s, dtype=d, device="cuda") for s, d in shapes for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(out, want) and len(others) == 12
+
+
+# -- far positions -----------------------------------------------------------------
+
+def exact_turns(pos, w):
+    """pos * w / (2 pi) less its whole turns, to 1e-17: the product in 60 digits."""
+    getcontext().prec = 60
+    inv = Decimal("0.15915494309189533576888376337251436203445964574045644874766734")
+    x = Decimal(int(pos)) * Decimal(float(w)) * inv
+    return float(x - x.to_integral_value())
+
+
+@pytest.mark.parametrize("hd, inter", [(64, False), (64, True), (66, False)])   # (66: the kernel for any size)
+def test_far_positions_keep_their_phase(hd, inter):
+    """Rows (1, 0) turn into the cosine and sine themselves (the products are exact).
+    The phase is rounded to fp32 once (at most 2^-26 turns, pi / 2 units of 2^-24
+    radians), sine and cosine are off by at most 2 units: 3.6 together, 4 allowed,
+    at every position an int32 holds."""
+    top = 1 << 31
+    pos = [0, 1, -1, 1 << 24, (1 << 27) - 5, -(1 << 29) + 3] + [top - 1 - 7919 * i for i in range(60)] + \
+        [-top + 104729 * i for i in range(60)]
+    w = freqs(64)[0].cpu()
+    x = torch.zeros(len(pos), 1, hd, device="cuda")
+    ia = torch.arange(0, 64, 2) if inter else torch.arange(32)
+    ib = ia + 1 if inter else ia + 32
+    x[..., ia] = 1.0
+    out = torch.empty_like(x)
+    dg.qk_norm_rope(x, None, i32(pos), out, None, rope=dg.Rope(w.cuda(), interleaved=inter))
+    turns = np.array([[exact_turns(p, f) for f in w] for p in pos])
+    got = out[:, 0].cpu().double().numpy()
+    for at, want in ((ia, np.cos(2 * np.pi * turns)), (ib, np.sin(2 * np.pi * turns))):
+        off = np.abs(got[:, at.numpy()] - want) * 2.0 ** 24
+        assert off.max() <= 4.0, off.max()
