@@ -312,3 +312,49 @@ def test_far_positions_keep_their_phase(hd, inter):
     for at, want in ((ia, np.cos(2 * np.pi * turns)), (ib, np.sin(2 * np.pi * turns))):
         off = np.abs(got[:, at.numpy()] - want) * 2.0 ** 24
         assert off.max() <= 4.0, off.max()
+
+
+# -- captured calls ----------------------------------------------------------------
+
+def test_a_replay_whose_token_has_no_slot():
+    """Lengths that change between replays, one of them below the count of new
+    tokens: that token is reported and not stored, and sees the prefix alone."""
+    b = Batch(91, BF, 2, 128, 16, [1, 1, 1], [600, 600, 600], 100)
+    rope, norm = dg.Rope(freqs(128)[0]), dg.HeadNorm(1e-6)
+    q, k, v = (randn(gen(i), 3, h, 128, dtype=BF) for i, h in ((1, 8), (2, 2), (3, 2)))
+    q2, out, lse, words = torch.empty_like(q), torch.empty_like(q), torch.empty(3, 8, device="cuda"), [i32([0]), i32([0])]
+    ws = torch.empty(dg.paged_attention_workspace(3, 8, 128, True), dtype=torch.uint8, device="cuda")
+
+    def step():
+        dg.paged_append(b.cache, b.batch, k, v, rope=rope, norm=norm, q=q, q_out=q2, status=words[0])
+        dg.paged_attention(b.cache, b.batch, q2, out, lse=lse, workspace=ws, status=words[1])
+
+    step()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    eps = float(np.float32(1e-6))
+    for kv in ([601, 17, 300], [128, 0, 129], [1, 2, 601]):
+        b.kv = kv
+        b.batch.kv_lens.copy_(i32(kv))
+        for t in (out, lse, q2):
+            t.fill_(9.0)
+        for t in words:
+            t.zero_()
+        k0, v0 = b.k.clone(), b.v.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(words[0]) == (5 if 0 in kv else 0) and int(words[1]) == 0
+        pos = torch.tensor([100 + n - 1 for n in kv], device="cuda")
+        near_turned(q2, *turned(q, pos, None, eps, rope.inv_freq))
+        kept = [i for i in range(3) if kv[i]]
+        at, off = torch.tensor([b.slots(i)[-1] for i in kept], device="cuda").t()
+        near_turned(b.k[at, :, off], *turned(k[kept], pos[kept], None, eps, rope.inv_freq))
+        assert torch.equal(b.v[at, :, off], v[kept])
+        k0[at, :, off], v0[at, :, off] = b.k[at, :, off], b.v[at, :, off]
+        assert torch.equal(b.k, k0) and torch.equal(b.v, v0)
+        want, want_lse, tol, tol_lse = attend(b, q2, True, float(np.float32(1 / math.sqrt(128))), BF)
+        assert torch.all((out.double() - want).abs() <= tol)
+        assert torch.all((lse.double() - want_lse).abs() <= tol_lse)
+    del graph
