@@ -267,7 +267,9 @@ typedef struct dg_paged_kv {
  * at offset j % page_size; entries past the last needed page are not read.
  * A prefix of prefix_len tokens in the pages prefix_pages precedes every
  * sequence (position = prefix_len + own token).  Rows outside
- * cu_q[0] .. cu_q[n_seqs] - 1 are neither read nor written. */
+ * cu_q[0] .. cu_q[n_seqs] - 1 are not written, and what they hold has no
+ * effect (their inputs may be read: the loads start before the sequence is
+ * known). */
 typedef struct dg_paged_batch {
   int32_t n_seqs, n_tokens;     /* n_tokens: rows of the token buffers            */
   const int32_t* cu_q;          /* device [n_seqs + 1], not decreasing            */

@@ -358,3 +358,32 @@ def test_a_replay_whose_token_has_no_slot():
         assert torch.all((out.double() - want).abs() <= tol)
         assert torch.all((lse.double() - want_lse).abs() <= tol_lse)
     del graph
+
+
+# -- rows of no sequence, slots given twice ----------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+def test_rows_of_no_sequence_are_not_written_and_have_no_effect(dtype):
+    """Spare rows before the first sequence and after the last."""
+    b = Batch(92, dtype, 2, 64, 16, [3, 0, 70], [20, 4, 9], prefix=33)
+    n = int(b.cu[-1])
+    batch = dg.PagedBatch(i32(b.cu + 4), i32(b.kv), i32(b.table), prefix_pages=i32(b.prefix_ids), prefix_len=b.prefix)
+    rope, norm = dg.Rope(freqs(64)[0]), dg.HeadNorm(1e-6)
+    x = [randn(gen(i), n + 9, h, 64, dtype=dtype) for i, h in ((1, 6), (2, 2), (3, 2))]
+    runs = []
+    for fill in (0.0, float("nan")):
+        q, k, v = (t.clone() for t in x)
+        for t in (q, k, v):
+            t[:4], t[4 + n:] = fill, fill
+        cache = dg.PagedKV(b.k.clone(), b.v.clone())
+        q2, out, lse = torch.full_like(q, 3.0), torch.full_like(q, 3.0), torch.full((n + 9, 6), 3.0, device="cuda")
+        word = i32([0])
+        dg.paged_append(cache, batch, k, v, rope=rope, norm=norm, q=q, q_out=q2, status=word)
+        dg.paged_attention(cache, batch, q2, out, lse=lse, status=word)
+        assert int(word) == 0
+        for t in (q2, out, lse):
+            assert torch.all(t[:4] == 3.0) and torch.all(t[4 + n:] == 3.0)
+        runs.append([cache.k, cache.v, q2, out, lse])
+    for a, c in zip(*runs):
+        assert torch.equal(a, c)
+    assert torch.all(torch.isfinite(runs[0][3].float()))
