@@ -296,8 +296,9 @@ dg_status dg_qk_norm_rope(int32_t dtype, int32_t n_tokens, int32_t n_heads, int3
  * slot the batch gives it.  With q (n_heads > 0) the same tokens' queries are
  * normalised and rotated into q_out in the same launch.  A token whose slot does
  * not exist (own token below 0, past max_pages, page id out of range) is not
- * stored and reported; the others keep theirs.  Two tokens with one slot: either
- * may win.  head_dim is even, 2 .. 256. */
+ * stored and reported; the others keep theirs.  Two tokens with one slot: every
+ * component there is one of theirs, not all need be of the same one.
+ * head_dim is even, 2 .. 256. */
 dg_status dg_paged_append(const dg_paged_kv* cache, const dg_paged_batch* batch, const dg_heads* k,
                           const dg_heads* v, const dg_rope* rope, const dg_head_norm* norm, int32_t n_heads,
                           const dg_heads* q, const dg_heads* q_out, int32_t* status_word, void* stream);

@@ -387,3 +387,16 @@ def test_rows_of_no_sequence_are_not_written_and_have_no_effect(dtype):
     for a, c in zip(*runs):
         assert torch.equal(a, c)
     assert torch.all(torch.isfinite(runs[0][3].float()))
+
+
+def test_a_slot_given_twice_holds_parts_of_its_tokens():
+    b = Batch(93, BF, 2, 64, 16, [1, 1], [5, 5])
+    table = np.tile(b.table[:1], (2, 1))
+    k, v = randn(gen(1), 2, 2, 64, dtype=BF), randn(gen(2), 2, 2, 64, dtype=BF)
+    k0, v0 = b.k.clone(), b.v.clone()
+    dg.paged_append(b.cache, dg.PagedBatch(i32([0, 1, 2]), i32([6, 6]), i32(table)), k, v)
+    at = int(table[0, 0])
+    for got, x in ((b.k[at, :, 5], k), (b.v[at, :, 5], v)):
+        assert torch.all((got == x[0]) | (got == x[1]))
+    k0[at, :, 5], v0[at, :, 5] = b.k[at, :, 5], b.v[at, :, 5]
+    assert torch.equal(b.k, k0) and torch.equal(b.v, v0)
