@@ -400,3 +400,27 @@ def test_a_slot_given_twice_holds_parts_of_its_tokens():
         assert torch.all((got == x[0]) | (got == x[1]))
     k0[at, :, 5], v0[at, :, 5] = b.k[at, :, 5], b.v[at, :, 5]
     assert torch.equal(b.k, k0) and torch.equal(b.v, v0)
+
+
+# -- kernel variants that only many rows reach -------------------------------------
+
+# (more than 148 x 32 batches of heads: the kernel of four groups a batch; more
+# heads of a kind than one of its batches holds, so a warp goes through several;
+# the last heads of a batch missing)
+@pytest.mark.parametrize("case", [
+    (BF, 1201, 40, 2, 128, 128, True, "fused"), (BF, 701, 37, 9, 128, 64, False, "own"),
+    (BF, 2500, 5, 1, 64, 32, True, "own"), (F32, 1301, 20, 4, 64, 32, True, "fused"),
+    (F32, 801, 18, 3, 128, 128, False, "own"), (F32, 1601, 9, 1, 128, 128, True, "own"),
+], ids=str)
+def test_norm_rope_of_many_rows(case):
+    base.test_norm_rope(case)
+
+
+@pytest.mark.parametrize("case", [
+    (BF, 20, 4, 128, 64, 128, True, [300, 501], [3, 0], 5),
+    (BF, 37, 17, 128, 16, 64, False, [257, 1, 200], [0, 90, 31], 0),
+    (F32, 19, 9, 64, 32, 32, True, [400, 300], [0, 17], 40),
+    (F32, 0, 20, 64, 64, 64, False, [600, 1], [5, 0], 0),
+], ids=lambda c: f"{len(c[7])}x{max(c[7])}-{c[1]}-{c[2]}-{c[3]}")
+def test_append_of_many_rows(case):
+    base.test_append(case)
