@@ -39,38 +39,61 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in SOURCES)
 
 
-def build_binding(force: bool = False) -> str:
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING)
-                                                     for s in BINDING_SOURCES):
-        return BINDING
+def _binding_paths():
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(cuda, "include")], os.path.join(root, "lib")
+
+
+def binding_lacks() -> str:
+    """Why the binding cannot be compiled here ("": it can).  libdg.so needs nvcc alone."""
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return "torch is not installed"
+    if shutil.which("g++") is None:
+        return "g++ is not installed"
+    dirs, lib = _binding_paths()
+    for f in ("c10/cuda/CUDAStream.h", "torch/csrc/autograd/python_variable.h", "Python.h", "cuda_runtime_api.h"):
+        if not any(os.path.exists(os.path.join(d, f)) for d in dirs):
+            return f"the header {f} is not installed"
+    return "" if os.path.exists(os.path.join(lib, "libc10_cuda.so")) else "torch has no CUDA library"
+
+
+def build_binding(force: bool = False) -> str:
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING)
+                                                     for s in BINDING_SOURCES):
+        return BINDING
+    import torch
+    dirs, lib = _binding_paths()
     tmp = BINDING + ".tmp%d" % os.getpid()
     subprocess.check_call(["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
                            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                           *["-I" + d for d in dirs], "-o", tmp, BINDING_SOURCES[0], "-L" + os.path.join(root, "lib"),
+                           *["-I" + d for d in dirs], "-o", tmp, BINDING_SOURCES[0], "-L" + lib,
                            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, lib: str = LIB) -> str:
+    if force or lib != LIB or stale():
+        tmp = lib + ".tmp%d" % os.getpid()
+        cmd = [nvcc(), "-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC", "-shared",
+               "-o", tmp, "--threads", "0", *(os.path.join(HERE, "csrc", f) for f in UNITS)]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        subprocess.check_call(cmd)
+        os.replace(tmp, lib)
     if lib == LIB:
-        build_binding(force)
-    if not force and lib == LIB and not stale():
-        return lib
-    tmp = lib + ".tmp%d" % os.getpid()
-    cmd = [nvcc(), "-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC", "-shared",
-           "-o", tmp, "--threads", "0", *(os.path.join(HERE, "csrc", f) for f in UNITS)]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
-    os.replace(tmp, lib)
+        lacks = binding_lacks()
+        if lacks:
+            print(f"the Python side of the serving operators is not built: {lacks}", file=sys.stderr)
+        else:
+            build_binding(force)
     return lib
 
 
