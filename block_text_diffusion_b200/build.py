@@ -20,8 +20,10 @@ UNITS = ("dg_engine.cu", "dg_noalloc.cu", "dg_serve.cu")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
-# The Python side of the serving operators: C++ against torch's headers.
+# The Python side of the serving operators: C++ against torch's headers.  Beside
+# it stands what it was compiled for: another torch or Python needs another one.
 BINDING = os.path.join(HERE, "_serving.so")
+BINDING_KEY = os.path.join(HERE, "_serving.key")
 BINDING_SOURCES = [os.path.join(HERE, "csrc", "dg_serving_py.cpp"), os.path.join(ROOT, "include", "dg.h")]
 
 
@@ -37,6 +39,20 @@ def stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(s) > t for s in SOURCES)
+
+
+def binding_key() -> str:
+    """What a compiled binding depends on besides its sources."""
+    import torch
+    return f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} python {sys.version.split()[0]}\n"
+
+
+def binding_built_for() -> str:
+    """The binding_key of the binding that is there ("" if unknown)."""
+    if not os.path.exists(BINDING_KEY):
+        return ""
+    with open(BINDING_KEY) as f:
+        return f.read()
 
 
 def _binding_paths():
@@ -65,8 +81,9 @@ def binding_lacks() -> str:
 
 
 def build_binding(force: bool = False) -> str:
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(s) <= os.path.getmtime(BINDING)
-                                                     for s in BINDING_SOURCES):
+    key = binding_key()
+    if not force and os.path.exists(BINDING) and binding_built_for() == key and all(
+            os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in BINDING_SOURCES):
         return BINDING
     import torch
     dirs, lib = _binding_paths()
@@ -76,6 +93,9 @@ def build_binding(force: bool = False) -> str:
                            *["-I" + d for d in dirs], "-o", tmp, BINDING_SOURCES[0], "-L" + lib,
                            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)
+    with open(BINDING_KEY + ".tmp%d" % os.getpid(), "w") as f:
+        f.write(key)
+    os.replace(f.name, BINDING_KEY)
     return BINDING
 
 

@@ -78,6 +78,10 @@ def _native():
         L = package.lib()
         if not os.path.exists(NATIVE_PATH):
             raise RuntimeError(f"{NATIVE_PATH} is missing: build it with `python -m block_text_diffusion_b200.build`")
+        from . import build
+        if build.binding_built_for() != build.binding_key():
+            raise RuntimeError(f"{NATIVE_PATH} was built for another torch or Python ({build.binding_built_for().strip()}): "
+                               "build it with `python -m block_text_diffusion_b200.build`")
         from . import _serving
         _serving.bind(*[ctypes.cast(getattr(L, n), _P).value for n in _NAMES], package.DGError)
         _bound = _serving
