@@ -280,7 +280,9 @@ def paged_append(cache, batch, k, v, rope=None, norm=None, q=None, q_out=None, s
 def paged_attention_workspace(n_tokens, n_heads, head_dim, with_prefix=False):
     """Bytes of workspace paged_attention needs for that many token rows."""
     from . import DGError, lib
-    n = int(lib().dg_paged_attention_workspace(n_tokens, n_heads, head_dim, int(bool(with_prefix))))
+    # (ctypes would take what does not fit an int32 modulo 2^32)
+    fits = all(0 <= x < 1 << 31 for x in (n_tokens, n_heads, head_dim))
+    n = int(lib().dg_paged_attention_workspace(n_tokens, n_heads, head_dim, int(bool(with_prefix)))) if fits else 0
     if n == 0:
         raise DGError(1, "dg_paged_attention_workspace")
     return n
