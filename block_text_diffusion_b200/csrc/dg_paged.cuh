@@ -40,7 +40,6 @@ constexpr int kStatusState = 5;     // DG_ERR_STATE
 DG_HD int imin(int a, int b) { return a < b ? a : b; }
 DG_HD int imax(int a, int b) { return a > b ? a : b; }
 DG_HD long long lmin(long long a, long long b) { return a < b ? a : b; }
-DG_HD long long lmax(long long a, long long b) { return a > b ? a : b; }
 
 DG_HD void paged_error(const PagedBatch& b, int code) {
 #ifdef __CUDA_ARCH__
