@@ -160,7 +160,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
   uint8_t* sStage = sKV + ST * C::kBytes;         // epilogue staging
   __shared__ __align__(8) uint64_t kv_full[ST], kv_empty[ST], frag_full[kPaFrags], frag_empty[kPaFrags];
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_part[2], p_full[2], o_done[2];
-  __shared__ __align__(8) uint64_t half_full, half_empty, v_last, v_tail[2], turn[2][4];
+  __shared__ __align__(8) uint64_t half_full, half_empty, v_last, v_tail[2], turn[2][4], mma_end[2];
   __shared__ PagedFrag s_frag[kPaFrags];
   __shared__ float s_half[128][2];                // split: maximum and sum of B's half, per row
   __shared__ uint32_t tmem_base;
@@ -180,6 +180,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       mbar_init(&p_part[t], 4);
       mbar_init(&p_full[t], 4);
       mbar_init(&o_done[t], 1);
+      mbar_init(&mma_end[t], 1);
     }
     mbar_init(&v_last, 2);
     mbar_init(&half_full, 4);
@@ -255,6 +256,11 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         __syncwarp();
       }
     }
+    // The ring's last loads have landed before the block gives its memory up.
+    // (They have long been used, unless a wait ran out somewhere.)
+#pragma unroll 1
+    for (int c = max(0, cnt - ST); c < cnt; ++c)
+      if (!pa_wait(&kv_full[c % ST], (c / ST) & 1, err)) break;
   } else if (warp == 9 || warp == 11) {
     // ---------------- MMA issue: warp 9 for A, warp 11 for B ----------------
     // One thread for each accumulator: what a thread does between two products
@@ -355,6 +361,9 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         while (ok && i < 2 * n) mbar_arrive(&kv_empty[step()]);
       }
+      // and so have this thread's products
+      tc_commit(&mma_end[t]);
+      pa_wait_one(&mma_end[t], 0, err);
     }
     __syncwarp();
   } else if (warp == 10) {
@@ -641,6 +650,7 @@ k_paged_attn_tc(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       tc_fence_before();
       if (both) warp_arrive(&half_empty);
     }
+    tmem_wait_st();   // (a wait that ran out leaves the loop between a store and its end)
   }
   tc_fence_before();
   __syncthreads();
