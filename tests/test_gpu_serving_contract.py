@@ -424,3 +424,50 @@ def test_norm_rope_of_many_rows(case):
 ], ids=lambda c: f"{len(c[7])}x{max(c[7])}-{c[1]}-{c[2]}-{c[3]}")
 def test_append_of_many_rows(case):
     base.test_append(case)
+
+
+# -- shapes the documentation allows and nothing above has -------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("hq, hk, hd", [(600, 1, 64), (1030, 2, 128)])
+def test_more_query_heads_than_a_tile_has_rows(dtype, hq, hk, hd):
+    b = Batch(94, dtype, hk, hd, 16, [2, 1, 3], [9, 200, 0], prefix=20, fill=float("nan"))
+    check_attention(b, randn(gen(1), b.rows, hq, hd, dtype=dtype, std=1.5), True, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("new", [[1] * 63 + [700], [1, 1, 1, 1500, 1]])
+def test_a_prompt_beside_single_tokens(dtype, new):
+    """In the tiles of 128 rows, which the average length asks for, and in those of 256."""
+    past = [37 * i % 500 for i in range(len(new))]
+    b = Batch(95, dtype, 2, 64, 32, new, past, prefix=100, fill=float("nan"))
+    check_attention(b, randn(gen(2), b.rows, 4, 64, dtype=dtype, std=1.5), True, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("prefix", [0, 150])
+def test_sequences_without_pages_of_their_own(dtype, causal, prefix):
+    b = Batch(96, dtype, 2, 64, 16, [300, 1], [-300, -1], prefix=prefix, fill=float("nan"))
+    b.batch = dg.PagedBatch(i32(b.cu), i32([0, 0]), torch.empty(2, 0, dtype=torch.int32, device="cuda"),
+                            prefix_pages=i32(b.prefix_ids) if prefix else None, prefix_len=prefix)
+    check_attention(b, randn(gen(3), b.rows, 4, 64, dtype=dtype), causal, dtype)
+
+
+@pytest.mark.parametrize("hd, rot", [(128, 128), (66, 20)])
+@pytest.mark.parametrize("tokens", [3, 900])
+def test_append_turns_queries_in_place_in_a_fused_projection(hd, rot, tokens):
+    b = Batch(97, BF, 3, hd, 16, [tokens, 1], [11, 30], prefix=5)
+    qkv = randn(gen(4), b.rows, 11 * hd, dtype=BF)
+    rope, norm = dg.Rope(freqs(rot)[0]), dg.HeadNorm(1e-6)
+    runs = []
+    for in_place in (False, True):
+        x = qkv.clone()
+        q, k, v = (t.view(b.rows, -1, hd) for t in x.split([5 * hd, 3 * hd, 3 * hd], dim=1))
+        out = q if in_place else torch.empty(b.rows, 5, hd, dtype=BF, device="cuda")
+        cache = dg.PagedKV(b.k.clone(), b.v.clone())
+        dg.paged_append(cache, b.batch, k, v, rope=rope, norm=norm, q=q, q_out=out)
+        assert torch.equal(x[:, 5 * hd:], qkv[:, 5 * hd:])
+        runs.append([out, cache.k, cache.v])
+    for a, c in zip(*runs):
+        assert torch.equal(a, c)
