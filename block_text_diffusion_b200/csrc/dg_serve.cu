@@ -87,10 +87,10 @@ bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 // Largest |offset| a row of heads reaches stays far inside 64 bits.  Buffers of
 // no rows may have no address.
-bool heads_ok(const dg_heads* h, int64_t n_tokens) {
+bool heads_ok(const dg_heads* h, int dtype, int64_t n_tokens) {
   const int64_t lim = (int64_t)1 << 40;
-  return h && (h->data || n_tokens == 0) && h->token_stride >= 0 && h->head_stride >= 0 && h->token_stride < lim &&
-         h->head_stride < lim;
+  return h && (h->data || n_tokens == 0) && aligned(h->data, elem_size(dtype)) && h->token_stride >= 0 &&
+         h->head_stride >= 0 && h->token_stride < lim && h->head_stride < lim;
 }
 
 bool rope_ok(const dg_rope* r, int head_dim) {
@@ -99,7 +99,10 @@ bool rope_ok(const dg_rope* r, int head_dim) {
   return r->rot_dim == 0 || (r->inv_freq && aligned(r->inv_freq, 8));
 }
 
-bool norm_ok(const dg_head_norm* n) { return !n || !n->enabled || n->eps >= 0.0f; }
+bool norm_ok(const dg_head_norm* n, int dtype) {
+  return !n || !n->enabled ||
+         (n->eps >= 0.0f && aligned(n->q_gain, elem_size(dtype)) && aligned(n->k_gain, elem_size(dtype)));
+}
 
 bool cache_ok(const dg_paged_kv* c) {
   if (!c || !c->k || !c->v || (c->dtype != DG_FP32 && c->dtype != DG_BF16)) return false;
@@ -112,6 +115,8 @@ bool cache_ok(const dg_paged_kv* c) {
 bool batch_ok(const dg_paged_kv* c, const dg_paged_batch* b) {
   if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->max_pages < 0 || b->prefix_len < 0) return false;
   if (b->n_seqs > 0 && (!b->cu_q || !b->kv_lens)) return false;
+  for (const int32_t* p : {b->cu_q, b->kv_lens, b->page_table, b->prefix_pages})
+    if (!aligned(p, 4)) return false;
   if (b->n_seqs > 0 && b->max_pages > 0 && (!b->page_table || b->table_stride < b->max_pages)) return false;
   // positions are int32
   if ((int64_t)b->prefix_len + (int64_t)b->max_pages * c->page_size >= (int64_t)1 << 31) return false;
@@ -268,10 +273,10 @@ extern "C" dg_status dg_qk_norm_rope(int32_t dtype, int32_t n_tokens, int32_t n_
                                      const dg_head_norm* norm, void* stream) {
   if ((dtype != DG_FP32 && dtype != DG_BF16) || n_tokens < 0 || n_heads < 0 || n_kv_heads < 0) return DG_ERR_INVALID_ARG;
   if (head_dim < 2 || head_dim > 256 || head_dim % 2) return DG_ERR_INVALID_ARG;
-  if (n_heads > 0 && (!heads_ok(q, n_tokens) || !heads_ok(q_out, n_tokens))) return DG_ERR_INVALID_ARG;
-  if (n_kv_heads > 0 && (!heads_ok(k, n_tokens) || !heads_ok(k_out, n_tokens))) return DG_ERR_INVALID_ARG;
+  if (n_heads > 0 && (!heads_ok(q, dtype, n_tokens) || !heads_ok(q_out, dtype, n_tokens))) return DG_ERR_INVALID_ARG;
+  if (n_kv_heads > 0 && (!heads_ok(k, dtype, n_tokens) || !heads_ok(k_out, dtype, n_tokens))) return DG_ERR_INVALID_ARG;
   if ((int64_t)n_heads + n_kv_heads > 65536) return DG_ERR_INVALID_ARG;
-  if (!rope_ok(rope, head_dim) || !norm_ok(norm)) return DG_ERR_INVALID_ARG;
+  if (!rope_ok(rope, head_dim) || !norm_ok(norm, dtype) || !aligned(positions, 4)) return DG_ERR_INVALID_ARG;
   if (rope && rope->rot_dim > 0 && !positions && n_tokens > 0) return DG_ERR_INVALID_ARG;
   HeadRowsArgs a{};
   a.n_tokens = n_tokens;
@@ -291,10 +296,11 @@ extern "C" dg_status dg_paged_append(const dg_paged_kv* cache, const dg_paged_ba
                                      int32_t* status_word, void* stream) {
   if (!cache_ok(cache) || !batch_ok(cache, batch)) return DG_ERR_INVALID_ARG;
   const int64_t rows = batch->n_tokens;
-  if (!heads_ok(k, rows) || !heads_ok(v, rows)) return DG_ERR_INVALID_ARG;
-  if (n_heads < 0 || (n_heads > 0 && (!heads_ok(q, rows) || !heads_ok(q_out, rows)))) return DG_ERR_INVALID_ARG;
+  const int dtype = cache->dtype;
+  if (!heads_ok(k, dtype, rows) || !heads_ok(v, dtype, rows) || !aligned(status_word, 4)) return DG_ERR_INVALID_ARG;
+  if (n_heads < 0 || (n_heads > 0 && (!heads_ok(q, dtype, rows) || !heads_ok(q_out, dtype, rows)))) return DG_ERR_INVALID_ARG;
   if ((int64_t)n_heads + 2ll * cache->n_kv_heads > 65536) return DG_ERR_INVALID_ARG;
-  if (!rope_ok(rope, cache->head_dim) || !norm_ok(norm)) return DG_ERR_INVALID_ARG;
+  if (!rope_ok(rope, cache->head_dim) || !norm_ok(norm, dtype)) return DG_ERR_INVALID_ARG;
   HeadRowsArgs a{};
   a.n_tokens = batch->n_seqs > 0 ? batch->n_tokens : 0;
   a.n_q = n_heads;
@@ -327,11 +333,13 @@ extern "C" dg_status dg_paged_attention(const dg_paged_kv* cache, const dg_paged
   if (hd != 64 && hd != 128) return DG_ERR_UNSUPPORTED;
   if (n_heads < 1 || n_heads > 32768 || n_heads % cache->n_kv_heads || !(scale > 0.0f) || scale > 1e30f) return DG_ERR_INVALID_ARG;
   const size_t need = dg_paged_attention_workspace(batch->n_tokens, n_heads, hd, batch->prefix_len > 0);
-  if (need == 0 || !workspace || workspace_bytes < need || !aligned(workspace, 256)) return DG_ERR_INVALID_ARG;
+  if (need == 0 || !workspace || workspace_bytes < need || !aligned(workspace, 256) || !aligned(lse, 4) ||
+      !aligned(status_word, 4))
+    return DG_ERR_INVALID_ARG;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return DG_OK;
   const int per16 = 16 / elem_size(cache->dtype);
   for (const dg_heads* h : {q, out})
-    if (!heads_ok(h, batch->n_tokens) || !aligned(h->data, 16) || h->token_stride % per16 || h->head_stride % per16)
+    if (!heads_ok(h, cache->dtype, batch->n_tokens) || !aligned(h->data, 16) || h->token_stride % per16 || h->head_stride % per16)
       return DG_ERR_INVALID_ARG;
   // The line of work units (see dg_paged_attn.cuh) is counted in 32 bits: at
   // most this many tiles of 64 rows, each with every block of 64 keys.

@@ -227,6 +227,7 @@ dg_status dg_gemm_splitk_noalloc(const void* A, const void* B, float* out, int32
  * outside the buffers it was given, whatever these arrays hold.
  *
  * Strides count elements.  The components of a head are always contiguous.
+ * Every pointer is a multiple of its element's size.
  * ------------------------------------------------------------------------- */
 
 /* Rows of heads: element (token, head, i) at data[token * token_stride + head * head_stride + i]. */
