@@ -73,17 +73,28 @@ def binding_lacks() -> str:
         return "torch is not installed"
     if shutil.which("g++") is None:
         return "g++ is not installed"
-    dirs, lib = _binding_paths()
+    try:
+        dirs, lib = _binding_paths()
+    except RuntimeError as e:
+        return str(e)
     for f in ("c10/cuda/CUDAStream.h", "torch/csrc/autograd/python_variable.h", "Python.h", "cuda_runtime_api.h"):
         if not any(os.path.exists(os.path.join(d, f)) for d in dirs):
             return f"the header {f} is not installed"
     return "" if os.path.exists(os.path.join(lib, "libc10_cuda.so")) else "torch has no CUDA library"
 
 
+def binding_fresh() -> bool:
+    """The binding is there, newer than its sources, and for this torch and Python."""
+    try:
+        key = binding_key()
+    except ImportError:
+        return False
+    return os.path.exists(BINDING) and binding_built_for() == key and all(
+        os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in BINDING_SOURCES)
+
+
 def build_binding(force: bool = False) -> str:
-    key = binding_key()
-    if not force and os.path.exists(BINDING) and binding_built_for() == key and all(
-            os.path.getmtime(s) <= os.path.getmtime(BINDING) for s in BINDING_SOURCES):
+    if not force and binding_fresh():
         return BINDING
     import torch
     dirs, lib = _binding_paths()
@@ -94,7 +105,7 @@ def build_binding(force: bool = False) -> str:
                            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)
     with open(BINDING_KEY + ".tmp%d" % os.getpid(), "w") as f:
-        f.write(key)
+        f.write(binding_key())
     os.replace(f.name, BINDING_KEY)
     return BINDING
 
@@ -108,12 +119,12 @@ def build(force: bool = False, verbose: bool = False, lib: str = LIB) -> str:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.check_call(cmd)
         os.replace(tmp, lib)
-    if lib == LIB:
+    if lib == LIB and (force or not binding_fresh()):
         lacks = binding_lacks()
         if lacks:
             print(f"the Python side of the serving operators is not built: {lacks}", file=sys.stderr)
         else:
-            build_binding(force)
+            build_binding(force=True)
     return lib
 
 

@@ -69,6 +69,25 @@ def test_the_binding_is_rebuilt_for_another_torch_or_python(tree, monkeypatch):
     assert calls == ["g++"] * 4
 
 
+def test_nothing_is_needed_where_all_is_built(tree, monkeypatch):
+    pytest.importorskip("torch")
+    b, calls = load(tree, monkeypatch)
+    monkeypatch.setenv("NVCC", str(tree / "nvcc"))
+    lacks = b.binding_lacks
+    monkeypatch.setattr(b, "binding_lacks", lambda: "")   # (the stand-in has no headers beside it)
+    b.build()
+    assert calls == [str(tree / "nvcc"), "g++"]
+
+    def missing():
+        raise RuntimeError("nvcc not found")
+
+    monkeypatch.setattr(b, "nvcc", missing)
+    monkeypatch.setattr(b, "binding_lacks", lacks)
+    assert b.build() == b.LIB and len(calls) == 2
+    os.remove(b.BINDING)
+    assert b.build() == b.LIB and len(calls) == 2   # a binding that cannot be compiled is no error
+
+
 def test_a_binding_for_another_torch_is_not_loaded(monkeypatch):
     pytest.importorskip("torch")
     from block_text_diffusion_b200 import build, serving
