@@ -105,8 +105,10 @@ __device__ __forceinline__ TokenSpot token_spot(const HeadRowsArgs& a, int t) {
 
 __device__ __forceinline__ void turn_sincos(int pos, double inv_freq, float amplitude, float& c, float& s) {
   constexpr double kTurn = 0.15915494309189533577, kTurnLo = -9.839338337591243e-18;   // 1 / (2 pi), and what that leaves
-  const double f = inv_freq * kTurn, f_lo = fma(inv_freq, kTurn, -f) + inv_freq * kTurnLo;
-  const double turns = pos * f, turns_lo = fma((double)pos, f, -turns) + pos * f_lo;
+  // (products by name: one that the compiler fused into the difference below
+  // would count its low part twice)
+  const double f = __dmul_rn(inv_freq, kTurn), f_lo = fma(inv_freq, kTurn, -f) + inv_freq * kTurnLo;
+  const double turns = __dmul_rn(pos, f), turns_lo = fma((double)pos, f, -turns) + pos * f_lo;
   const float r = (float)((turns - rint(turns)) + turns_lo);
   sincospif(2.0f * r, &s, &c);
   c *= amplitude;
