@@ -152,7 +152,10 @@ def test_tensors_reshaped_in_place_are_refused():
 # -- errors nobody gave a word for -------------------------------------------------
 
 def test_errors_without_a_status_word_are_kept_for_serving_status():
-    dg.serving_status()   # whatever earlier calls left
+    try:
+        dg.serving_status()
+    except dg.DGError:   # what earlier tests' calls left
+        pass
     b = Batch(85, BF, 2, 64, 16, [1, 1], [40, 40], prefix=20)
     q, k = randn(gen(1), 2, 4, 64, dtype=BF), randn(gen(2), 2, 2, 64, dtype=BF)
     out = torch.empty_like(q)
