@@ -116,7 +116,9 @@ __device__ __forceinline__ void turn_sincos(int pos, double inv_freq, float ampl
 }
 
 // Any head_dim, stride and alignment: one warp per head, a lane takes the
-// pairs lane, lane + 32, ...
+// pairs lane, lane + 32, ...  One value a load, and the angles of a token once
+// for every head: 8192 tokens of 24 bf16 heads of 96 take 93 us, of 128 with 24
+// components turned 87, where the kernel of whole chunks takes 20 for 128.
 constexpr int kHeadPairs = 4;   // head_dim <= 256: at most 4 pairs a lane
 
 template <typename T>
@@ -255,9 +257,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // is asked for before the sequence is looked up, so the chain of dependent
 // loads is the batch's alone.
 //
-// Many tokens: 4.6 TB/s (101 MB, 22.1 us among others) and 5.5 (268 MB, 48.4 us),
-// the instructions (1320 a warp) at 16 warps an SM being what is left; few: the
-// launch and two dependent reads (3.3 us).
+// Many tokens: 4.6 TB/s (101 MB, 22.0 us among others) and 5.3 (268 MB, 50.7 us),
+// bound by the latency of the loads: 114 registers leave 16 to 17 warps an SM,
+// and their 1300 or so instructions fill under half of the issue slots.  Few: the
+// launch and two dependent reads (3.1 to 3.6 us).
 template <typename T, int kGroups, bool kInter>
 __global__ void __launch_bounds__(32, 16) k_head_rows(const __grid_constant__ HeadRowsArgs a, int lph_shift,
                                                       unsigned warps_per_token, int batches_per_warp) {

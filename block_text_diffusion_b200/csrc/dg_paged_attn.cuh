@@ -81,7 +81,12 @@ struct PagedFrag {
 // tiles): 2 units 285 us, 3 to 5 263 us; ragged causal prompts 129, 128.5,
 // 125 and 123 us for 2, 3, 4 and 5; 64 single tokens (128-row tiles, bound by
 // memory, which a tile's start and end hardly hold up): 4 units 90.0 us,
-// 3 86.7, 2 85.1, 1 84.9.
+// 3 86.7, 2 85.1, 1 84.9.  Twice or three times as many 256-row tiles of 1 to 16
+// blocks on every CTA cost 10 to 14 us a tile beside 2.2 us a block, which is
+// the 5.  The fp32 tiles of 64 rows took the 2 over from the 128-row ones, where
+// a tile costs 7 us beside 5.5 us a block of 64 keys of 64: four causal prompts of
+// 512 tokens (8 heads of 128) take 94 us with 0, 98 with 1, 107 with 2 and 3,
+// 125 with 5; a canvas of 256 tokens 14 with 0 to 3, 18.5 with 5.
 constexpr int paged_tile_cost(int rows) { return rows == 256 ? 5 : 2; }
 
 template <int kRows, int kBlk>
@@ -522,12 +527,16 @@ k_paged_join(const __grid_constant__ PagedAttnArgs a, int row_shift, int grid_ma
 // At most 8 rows (single tokens): that mapping would leave seven of eight
 // warps without a row, so a thread takes the scores of one key for two rows,
 // and warp r then has row r for the softmax and the product with V.  Bound by
-// memory.
+// memory: 16 tokens over 2000 keys of 128, 1 to 8 rows a key head, 28 to 40 us,
+// with the other mapping 55 to 57.
 //
 // Measured, with the join: a canvas of 256 tokens (4 heads of 64, 64 keys
-// before it, 84 MFLOP) 14.4 us, of which the loads that depend on one another
+// before it, 84 MFLOP) 14.3 us, of which the loads that depend on one another
 // (lengths, pages, keys) and the second launch are most; the single mapping
-// without the double buffer took 16.7.
+// without the double buffer took 16.7.  Four causal prompts of 512 tokens (8
+// heads of 128) 107 us, 8 canvases of 256 behind a shared 1024-token prompt (8
+// heads of 128 over 2) 371: 20 and 29 TFLOP/s of a nominal 74, the FMA pipe busy
+// for 48 % of the former; a thread's 4 x 4 scores read 8 values for 16 products.
 // ---------------------------------------------------------------------------
 constexpr int kPaF32Rows = 64, kPaF32Blk = 64, kPaF32Few = 8;
 template <int kHd>

@@ -177,7 +177,13 @@ dg_status run_head_rows(const HeadRowsArgs& a, cudaStream_t s) {
   while ((1 << shift) < lph) ++shift;
   // Batches of `groups` x 32 / lph heads of one kind; a warp takes one batch
   // while the batches do not fill the SMs, all of its token's when they do
-  // (its sines and cosines then serve every head).
+  // (its sines and cosines then serve every head).  One batch against all, us
+  // (bf16, 16 + 8 heads of 128, 6 batches a token): 128 tokens 2.4 and 3.4, 256
+  // 2.8 and 3.4, 400 4.2 and 3.7, 789 5.6 and 3.9, 8192 53 and 20; (fp32, 4 + 4
+  // of 64, 2 batches) 1001 tokens 3.0 and 3.2, 1500 3.6 and 3.4, 2300 5.2 and
+  // 4.2.  The sides meet between 1500 and 3000 batches, where the warps no
+  // longer fit at once; from there to the 4736 of this rule one batch a warp
+  // costs up to 1.7 us more.
   const int hpw = 32 / lph;
   auto batches = [&](int groups) {
     auto of = [&](int n) { return (n + hpw * groups - 1) / (hpw * groups); };
@@ -229,7 +235,9 @@ dg_status run_join(const PagedAttnArgs& a, int tile, cudaStream_t s) {
   const long long rows = (long long)a.b.n_tokens * a.n_heads;
   int shift = 0;   // (tiles have 2^shift rows)
   while ((1 << shift) < tile) ++shift;
-  // a block per row while the rows do not fill the SMs
+  // A block per row while the rows do not fill the SMs: one token over 32768 keys
+  // with 8 to 128 heads 16.8 to 18.5 us for the call, 27.9 to 43.3 without; up to
+  // four rows an SM neither side wins (8 to 16 tokens of 16 heads: within 3 %).
   if (rows <= kSMs) return done(launch(k_paged_join<T, kHd, 16>, (unsigned)rows, 256, 0, s, a, shift, (int)kSMs, 1));
   const int per_block = (int)std::min<long long>(kJoinRows, (rows / (kSMs * 5) + 16) / 16 * 16);
   return done(launch(k_paged_join<T, kHd, 1>, (unsigned)((rows + per_block - 1) / per_block), 256, 0, s, a, shift,
@@ -248,7 +256,12 @@ template <int kHd>
 dg_status run_paged_attention(const dg_paged_kv* c, PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e;
   // Tiles of 128 rows where the average sequence has no more (single tokens);
-  // the lengths themselves are on the device.
+  // the lengths themselves are on the device.  128-row against 256-row tiles, us
+  // (16 heads of 128 over 8): 16 sequences of 16 rows a key head after 1000 keys
+  // 24.7 and 28.9, of 128 rows 32.9 and 36.4, of 256 rows 55.4 and 52.6.  Uneven
+  // batches: 63 single tokens after 1500 keys beside a prompt of 700 tokens 102
+  // and 128, of 4000 184 and 223 (128-row by this rule); 7 of them beside a
+  // prompt of 2048 57.1 and 63.3, and there the rule takes the slower 256.
   const bool narrow = (long long)a.b.n_tokens * a.G <= 128ll * a.b.n_seqs;
   if (c->dtype == DG_BF16) {
     CUtensorMap tk, tv;
