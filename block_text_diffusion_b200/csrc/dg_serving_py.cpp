@@ -41,7 +41,7 @@ struct Refused {};   // a Python exception is set
 // Interned attribute names.
 #define DG_NAMES(X)                                                                                                 \
   X(_at) X(index) X(inv_freq) X(q_gain) X(k_gain) X(k) X(v) X(cu_q) X(kv_lens) X(page_table) X(prefix_pages) X(_words) \
-  X(_tensors) X(cuda_stream) X(device)
+  X(cuda_stream) X(device)
 #define X(n) PyObject* s_##n;
 DG_NAMES(X)
 #undef X
@@ -152,11 +152,14 @@ struct Cache {
   const dg_paged_kv* c;
   at::ScalarType type;
   int index;
+  PyObject *k, *v;   // the cache's, which lives as long as the call
 };
 Cache cache_of(PyObject* o) {
   Cache r;
   Ref k(PyObject_GetAttr(o, s_k)), v(PyObject_GetAttr(o, s_v));   // (only a PagedKV has them)
   r.c = reinterpret_cast<const dg_paged_kv*>(attr_int(o, s__at));
+  r.k = k.p;
+  r.v = v.p;
   r.index = (int)attr_int(o, s_index);
   r.type = r.c->dtype == DG_BF16 ? at::kBFloat16 : at::kFloat;
   const int64_t shape[4] = {r.c->n_pages, r.c->n_kv_heads, r.c->page_size, r.c->head_dim};
@@ -166,11 +169,10 @@ Cache cache_of(PyObject* o) {
 }
 
 dg_paged_batch batch_of(PyObject* o, const Cache& c, int64_t tokens) {
-  Ref w(PyObject_GetAttr(o, s__words));   // index, n_seqs, the addresses, entries of prefix_pages
-  Ref ts(PyObject_GetAttr(o, s__tensors));
+  // index, n_seqs, the addresses, entries of prefix_pages; the four tensors
+  Ref w(PyObject_GetAttr(o, s__words));
   long long v[10];
-  if (!PyTuple_Check(w.p) || PyTuple_GET_SIZE(w.p) != 10 || !PyTuple_Check(ts.p) || PyTuple_GET_SIZE(ts.p) != 4)
-    refuse("batch must be a PagedBatch");
+  if (!PyTuple_Check(w.p) || PyTuple_GET_SIZE(w.p) != 14) refuse("batch must be a PagedBatch");
   for (int i = 0; i < 10; ++i) {
     v[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(w.p, i));
     if (v[i] == -1 && PyErr_Occurred()) throw Refused{};
@@ -190,7 +192,7 @@ dg_paged_batch batch_of(PyObject* o, const Cache& c, int64_t tokens) {
   // every tensor still has the memory and the shape that were noted (a table
   // that grew in place moved, and the old memory belongs to someone else)
   auto same = [&](int i, const char* name, const void* noted, at::IntArrayRef shape, bool contiguous) -> const at::Tensor& {
-    return check(held(PyTuple_GET_ITEM(ts.p, i), name, noted), name, at::kInt, shape, c.index, contiguous);
+    return check(held(PyTuple_GET_ITEM(w.p, 10 + i), name, noted), name, at::kInt, shape, c.index, contiguous);
   };
   const int64_t offsets = v[1] + 1, seqs = v[1], table[2] = {v[1], v[6]}, prefix = v[9];
   same(0, "cu_q", b.cu_q, at::IntArrayRef(&offsets, 1), true);
@@ -341,13 +343,13 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* status = status_of(a[8], c.index);
     On on(c.index, a[9]);
     for (int i : {2, 3, 6, 7, 8}) on.uses(a[i]);
-    on.uses(a[0], {s_k, s_v});
+    on.uses(c.k);
+    on.uses(c.v);
     on.uses(a[1], {s_cu_q, s_kv_lens, s_page_table, s_prefix_pages});
     on.uses(a[4], {s_inv_freq});
     on.uses(a[5], {s_q_gain, s_k_gain});
-    Ref k_pages(PyObject_GetAttr(a[0], s_k)), v_pages(PyObject_GetAttr(a[0], s_v));
     return finish(g.append(c.c, &b, &kr, &vr, rope, norm, (int32_t)hq, &qr, &qo, status, on.stream), "dg_paged_append",
-                  {k_pages.p, v_pages.p, a[7], a[8]});
+                  {c.k, c.v, a[7], a[8]});
   });
 }
 
@@ -386,7 +388,8 @@ PyObject* py_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("workspace must be a contiguous 1-D uint8 tensor on cuda:%d", c.index);
     On on(c.index, a[9]);
     for (int i : {2, 3, 6, 7, 8}) on.uses(a[i]);
-    on.uses(a[0], {s_k, s_v});
+    on.uses(c.k);
+    on.uses(c.v);
     on.uses(a[1], {s_cu_q, s_kv_lens, s_page_table, s_prefix_pages});
     return finish(g.attention(c.c, &b, (int32_t)hq, &qr, (float)scale, causal, &o, lse, ws.data_ptr(),
                               (size_t)ws.numel(), status, on.stream),

@@ -250,12 +250,11 @@ class PagedBatch(_Fixed):
         self.cu_q, self.kv_lens, self.page_table, self.prefix_pages = cu_q, kv_lens, page_table, prefix_pages
         self.n_seqs, self.prefix_len, self.index = n, int(prefix_len), cu_q.get_device()
         # what dg_paged_batch needs, and the tensors it comes from (each call checks that they did not move)
-        self._tensors = (cu_q, kv_lens, page_table, prefix_pages)
         self._args = (cu_q, kv_lens, page_table, prefix_pages, prefix_len)
         self._words = (self.index, n, cu_q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
                        max(page_table.stride(0), page_table.shape[1]), page_table.shape[1],
                        prefix_pages.data_ptr() if prefix_len else 0, int(prefix_len),
-                       prefix_pages.numel() if prefix_len else 0)
+                       prefix_pages.numel() if prefix_len else 0, cu_q, kv_lens, page_table, prefix_pages)
         self._fixed = True
 
 
